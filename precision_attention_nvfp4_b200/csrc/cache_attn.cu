@@ -631,9 +631,10 @@ __device__ __forceinline__ void load_tiles(const Params& p, uint8_t* smem, const
       if (gg >= C::kStages) wait.warp(empty + st, par, is_v ? kErrVEmpty : kErrKEmpty);
       if (!wait.dead) {
         if (elected) {
-          mbar_arrive_expect_tx(full + st, __popc(have) * page_bytes);
+          // before the arrival, which releases them to those who wait for the tile
           if (is_v && !scales) good[st] = have;
           issued[is_v] = gg + 1;
+          mbar_arrive_expect_tx(full + st, __popc(have) * page_bytes);
         }
         uint32_t dst = smem_u32(ring + st * C::kTile);
         for (int x = 0; x < ppt; ++x, dst += page_bytes) {
