@@ -625,10 +625,12 @@ typedef struct {
  *   causal, no mask  j <= L - n + i
  *   neither          j < L
  * K and V enter with the values the cache holds; Q in two E4M3 terms at a
- * power-of-two scale a row (its 8 bits, to 2^-18 of the row's largest), P in
- * an E4M3 and an E5M2 term (2^-7 relative down to 2^-10 of the row's largest P,
- * 2^-3 below; nothing under 2^-28 of it where a KV head has at most 32 query
- * rows (max_queries * Hq / H), 2^-21 where it has more), sums in fp32.
+ * power-of-two scale a row (its 8 bits, to 2^-18 of the row's largest). P is
+ * rounded after it was multiplied by the power of two of its V row, e: to 2^-9
+ * of its value where a KV head has at most 32 query rows (max_queries * Hq / H),
+ * to 2^-11 where it has more, down to 2^-24 of the row's largest p e; below, a
+ * p e is off by at most 2^-33 (2^-35) of that. Sums, the row sum among them
+ * (of P before it was rounded), in fp32.
  * A page of the table outside the cache, and a length beyond the table, count
  * as tokens that nobody sees. A query that sees no token gets out = 0 and
  * lse = -inf. A NaN row of the cache makes NaN the results of the queries that

@@ -7,17 +7,19 @@
 // query rows, so the products are laid out with the keys, not the queries, on
 // the tensor core's 128 rows: S^T = K Q^T has 128 keys by N query rows, O^T =
 // V^T P^T has d channels by N query rows (N = 16 or 32: the queries and heads that
-// share a KV head; for more rows see the kernel further down). K and V go from the cache to the MMA as
-// they are, E4M3 bytes moved by TMA; nothing is converted on the way. What
+// share a KV head; for more rows see the kernel further down). K and V go from the
+// cache to the MMA as they are, E4M3 bytes moved by TMA; nothing is converted on the way. What
 // has to stay precise is split instead, at N rows it is nearly free:
 //   Q = Qhi + Qlo, both E4M3 at a power-of-two scale a row: the 8 bits of a
 //     bf16 value exactly, to 2^-10 of a scale that brings the row to 224..448;
 //     both products go to one accumulator
-//   P = Phi + 2^-11 Plo, E4M3 and E5M2: 4 and 3 bits, 2^-7 relative, with a
-//     floor near 2^-31 of the largest P, so that very many small P against a
-//     few large ones keep their weight; two accumulators, added at the end
+//   P = P1 + 2^-3 P2 + 2^-7 P3, all E5M2 (3 bits each): 2^-9 of the value. The terms lie side
+//     by side in 3 N columns of one product, which reads V once, into three
+//     accumulators that are added at the end
 // The rows' scales are powers of two: K's multiplies its scores, V's is added to the
-// exponent of P, so that P V needs no scale, and taken out of the row sum.
+// exponent of P, so that P V needs no scale, and taken out of the row sum. So what is split
+// is P 2^ev, 2^10 or more for the row's largest: 2^-9 of it down to 2^-24 of the largest,
+// below that an error of at most 2^-33 of the largest.
 //
 // CTA (persistent, one an SM, 640 threads):
 //   warps 0, 3   TMA: K, and V with the scales, in 128-key tiles into two rings, page by page
@@ -28,8 +30,8 @@
 //                turn), with their own reference maxima, row sums and O, so that
 //                none waits on another; joined at a segment's end. They also
 //                load, scale and split the query rows of the next segment
-// The reference maximum of a row moves only when P would pass E4M3's largest,
-// and then goes 2^2 above that score, so that it seldom moves again; the 128
+// The reference maximum of a row moves only when P would pass E5M2's largest,
+// and P is 2^10 then, so that it seldom moves again; the 128
 // threads of a warpgroup agree on it with one barrier a group of rows, and O in
 // tensor memory is rescaled only then.
 //
@@ -66,14 +68,14 @@ constexpr int kSegs = 64;           // segments a CTA plans at a time
 // 4, 506 at 6, 512 at 8.
 template <int N>
 constexpr int kSegCost = N == 128 ? 6 : 8;
-constexpr float kPLog2 = 6.f;       // P is held at 2^6
-constexpr float kPTop = 8.8073549f;  // log2 448: P above it moves the reference maximum
-// A reference that moves goes this far above the score that moved it, so that it moves less often. No more than noise
-// where there are few rows (190.6 us without, 190 with, on the batch above); with many a tree of 61 tokens on 8
-// sequences of 16384 takes 166 us against 172 without.
-constexpr float kHeadroom = 2.f;
-constexpr float kWideHeadroom = 1.f;
-constexpr float kLoScale = 2048.f;  // Plo = 2^11 (P - Phi): at most 16 * 2^11 < E5M2's largest
+// A P above 2^kPTop moves the reference maximum, and is 2^kPLog2 then: the further apart, the less often, and the less of
+// P's range lies below. (Trees of 8 tokens on 8 sequences of up to 16384, 32 rows a KV head: 60 us with 13, 54 with 11,
+// 49 with 10, 48 with 9; 64 sequences of up to 2048, one token: 50, 49, 47 and 46.) kPTop is below the largest E5M2
+// (57344) and fp16.
+constexpr float kPLog2 = 10.f;
+constexpr float kPTop = 15.75f;
+// What P1 leaves is at most 2^12, what P2 leaves of that 2^8: scaled into E5M2's range, the terms reach further down.
+constexpr float kMidScale = 8.f, kLoScale = 128.f;
 constexpr float kNever = -1e30f;    // reference maximum before any key was seen
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -88,11 +90,10 @@ enum : int {
 // ---------------------------------------------------------------------------
 // Instructions
 // ---------------------------------------------------------------------------
-// kind::f8f6f4 descriptor, F32 accumulate; type 0 E4M3, 1 E5M2; major 1: MN.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int b_type, int a_mn, int b_mn, int a_type = 0) {
-  return (1u << 4) | (static_cast<uint32_t>(a_type) << 7) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
-         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
+// Descriptor with F32 accumulate; type 0: E4M3 of kind::f8f6f4, fp16 of kind::f16, 1: E5M2. major 1: MN.
+__host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn, int b_type = 0) {
+  return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t swz_of(int row_bytes) { return row_bytes == 128 ? 2u : (row_bytes == 64 ? 4u : 6u); }
 // 16-byte chunks of a row permuted as the 128-, 64- or 32-byte swizzle does.
@@ -154,6 +155,16 @@ __device__ __forceinline__ float redux_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16 (fp16 x fp16 -> F32); A is K-major in TMEM, two values a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // Barrier of `n` threads; every thread of them always takes part (see the loops).
 __device__ __forceinline__ void named_sync(int id, int n) {
   __syncwarp();
@@ -170,28 +181,71 @@ __device__ __forceinline__ bool named_any(int id, int n, bool x) {
       : "memory");
   return y != 0;
 }
-// Four P as E4M3 codes, and 2^11 times what they leave as E5M2 codes. (One
-// block: the 16-bit halves are then packed by the conversions themselves.)
-__device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
+// Four P as three E5M2 codes each: hi + mid / kMidScale + lo / kLoScale. (E5M2 is fp16's upper byte, so what a term
+// leaves is exact in fp16. One block: the 16-bit halves are then packed by the conversions themselves.)
+__device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   asm("{\n\t"
-      ".reg .b16 a, b, c, d;\n\t"
+      ".reg .b16 a, b;\n\t"
       ".reg .b32 h0, h1, r0, r1;\n\t"
-      "cvt.rn.f16x2.f32 h0, %3, %2;\n\t"
-      "cvt.rn.f16x2.f32 h1, %5, %4;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 a, h0;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 b, h1;\n\t"
+      "cvt.rn.f16x2.f32 h0, %4, %3;\n\t"
+      "cvt.rn.f16x2.f32 h1, %6, %5;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 a, h0;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 b, h1;\n\t"
       "mov.b32 %0, {a, b};\n\t"
-      "cvt.rn.f16x2.e4m3x2 r0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 r1, b;\n\t"
-      "sub.rn.f16x2 r0, h0, r0;\n\t"
-      "sub.rn.f16x2 r1, h1, r1;\n\t"
-      "mul.rn.f16x2 r0, r0, %6;\n\t"
-      "mul.rn.f16x2 r1, r1, %6;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 c, r0;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 d, r1;\n\t"
-      "mov.b32 %1, {c, d};\n\t}"
-      : "=r"(hi), "=r"(lo)
-      : "f"(p0), "f"(p1), "f"(p2), "f"(p3), "r"(0x68006800u));  // 2048 twice, kLoScale
+      "prmt.b32 r0, %0, 0, 0x1404;\n\t"
+      "prmt.b32 r1, %0, 0, 0x3424;\n\t"
+      "sub.rn.f16x2 h0, h0, r0;\n\t"
+      "sub.rn.f16x2 h1, h1, r1;\n\t"
+      "mul.rn.f16x2 h0, h0, %7;\n\t"
+      "mul.rn.f16x2 h1, h1, %7;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 a, h0;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 b, h1;\n\t"
+      "mov.b32 %1, {a, b};\n\t"
+      "prmt.b32 r0, %1, 0, 0x1404;\n\t"
+      "prmt.b32 r1, %1, 0, 0x3424;\n\t"
+      "sub.rn.f16x2 h0, h0, r0;\n\t"
+      "sub.rn.f16x2 h1, h1, r1;\n\t"
+      "mul.rn.f16x2 h0, h0, %8;\n\t"
+      "mul.rn.f16x2 h1, h1, %8;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 a, h0;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 b, h1;\n\t"
+      "mov.b32 %2, {a, b};\n\t}"
+      : "=&r"(hi), "=&r"(mid), "=r"(lo)
+      : "f"(p0), "f"(p1), "f"(p2), "f"(p3), "r"(0x48004800u), "r"(0x4C004C00u));  // twice 8, kMidScale; 16, the rest
+}
+// Two P as packed fp16.
+__device__ __forceinline__ uint32_t half_p(float p0, float p1) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(h) : "f"(p0), "f"(p1));
+  return h;
+}
+// Four E4M3 codes as fp16 (exact).
+__device__ __forceinline__ uint2 widen4(uint32_t codes) {
+  uint2 h;
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(h.x), "=r"(h.y)
+      : "r"(codes));
+  return h;
+}
+// A key's V row from the tile as TMA laid it out to a tile of fp16: [64 channels][128 keys][128 bytes], 128-byte swizzle.
+// Zeros where the key is not there: what lies behind a sequence, or in a page that is not there, may be NaN, and
+// 0 * NaN would reach O. (Eight lanes take eight keys' same 16 channels: no bank conflicts on either side.)
+template <int D, int kChunks>
+__device__ __forceinline__ void widen_row(const uint8_t* tile, uint8_t* wide, int key, int c0, bool live) {
+  const uint32_t keep = live ? ~0u : 0u;
+  uint4 x[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) x[c] = *reinterpret_cast<const uint4*>(tile + swizzled<D>(key * D + (c0 + c) * 16));
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) {
+    const uint2 a = widen4(x[c].x & keep), b = widen4(x[c].y & keep), e = widen4(x[c].z & keep), f = widen4(x[c].w & keep);
+    uint8_t* dst = wide + ((c0 + c) / 4) * 128 * 128;
+    *reinterpret_cast<uint4*>(dst + swizzled<128>(key * 128 + ((c0 + c) % 4) * 32)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(dst + swizzled<128>(key * 128 + ((c0 + c) % 4) * 32 + 16)) = make_uint4(e.x, e.y, f.x, f.y);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -212,9 +266,8 @@ struct Cfg {
   // tokens: 146 us with four and one, 152 with two and two; at 128 channels 178 and 177, one sequence of 131072 58
   // and 56).
   static constexpr int kPar = N == 16 && D == 64 ? 4 : 2, kHalves = 4 / kPar;
-  static constexpr int kPP = N < 32 ? 32 : N;              // row pitch of a P tile
-  static constexpr int kPLo = N == 16 ? 16 : 128 * kPP;    // the second term: beside the first, or behind it
-  static constexpr int kPTile = N == 16 ? 128 * kPP : 2 * 128 * kPP;
+  static constexpr int kPP = 4 * N;                        // row pitch of a P tile: a key's three terms, N bytes each
+  static constexpr int kPTile = 128 * kPP;
   static constexpr int kQ = N * D;                         // bytes of one term of Q
   static constexpr int kFixed = 2 * 2 * kQ + kPar * kPTile + 1024 * 8;
   static constexpr int kRoom = (227 * 1024 - 1024 - kFixed) / (2 * kTile + 256);
@@ -222,8 +275,8 @@ struct Cfg {
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffQ = kOffV + kStages * kTile;    // [2 buffers][2 terms][N][D]
-  static constexpr int kOffP = kOffQ + 4 * kQ;             // [kPar][128 keys, two terms]
-  static constexpr int kOffE = kOffP + kPar * kPTile;         // [stage][pages of the tile][2][page]: scales
+  static constexpr int kOffP = kOffQ + 4 * kQ;             // [kPar][128 keys][3 terms][N]
+  static constexpr int kOffE = kOffP + kPar * kPTile;      // [stage][pages of the tile][2][page]: scales
   static constexpr int kOffSeg = kOffE + kStages * 256;
   static constexpr int kOffF = kOffSeg + kSegs * static_cast<int>(sizeof(Seg));
   // 4-byte words: qmul [2][N], nbias [2 segments][kPar][N], wmax [kPar][4][N], lsum [2 segments][kPar][4][N],
@@ -239,9 +292,9 @@ struct Cfg {
   static constexpr int kBytes = kOffScan + 2 * 32 * 4 + 4 * kStages;
   static constexpr int kSmem = kBytes + 1024;
   static_assert(kSmem <= 227 * 1024 && kStages >= 3 && kStages >= kPar, "shared memory");
-  // tensor memory: S [kPar][N], O [kPar][hi, lo][N], row sums of every lane's keys [kPar][N]
-  static constexpr int kColS = 0, kColO = kPar * N, kColL = 3 * kPar * N;
-  static constexpr int kCols = 4 * kPar * N;
+  // tensor memory: S [kPar][N], O [kPar][3 terms][N], row sums of every lane's keys [kPar][N]
+  static constexpr int kColS = 0, kColO = kPar * N, kColL = 4 * kPar * N;
+  static constexpr int kCols = 8 * kPar * N;
   static constexpr int kHalf = N / kHalves;                     // query rows of a softmax warpgroup
   static constexpr int kGroup = N == 16 ? 8 : 16;   // of them, held by a thread at once
 };
@@ -300,6 +353,9 @@ __device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
+// kCall: the slow path is a call, so that it takes no room where warps are many; not in a kernel that moves registers
+// between its warps, whose calls would fix their number.
+template <bool kCall>
 struct Waiter {
   volatile int* abort;
   bool dead = false;
@@ -307,9 +363,10 @@ struct Waiter {
   __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity, int code) {
     const bool ok = try_wait(smem_u32(bar), parity);
     if (__all_sync(0xffffffffu, ok)) return true;
-    return slow(smem_u32(bar), parity, code);
+    return kCall ? called(smem_u32(bar), parity, code) : slow(smem_u32(bar), parity, code);
   }
-  __device__ __noinline__ bool slow(uint32_t addr, uint32_t parity, int code) {
+  __device__ __noinline__ bool called(uint32_t addr, uint32_t parity, int code) { return slow(addr, parity, code); }
+  __device__ __forceinline__ bool slow(uint32_t addr, uint32_t parity, int code) {
     if (dead) return false;
     const unsigned long long t0 = globaltimer_ns();
     for (;;) {
@@ -410,7 +467,7 @@ __device__ __forceinline__ void split_rows(const Params& p, const Seg& s, uint8_
 
 // Moves the references of rows c0 .. c0 + kG - 1 of a tile (parity w, called by
 // the 128 threads of a warpgroup) where a score passed them: those rows take the
-// tile's maximum and some headroom, and their sums and O (when there is one)
+// tile's maximum, and their sums and O (when there is one)
 // are rescaled. Out of line: few tiles need it, and its registers would crowd
 // the common path's (752 instead of 579 instructions a warp and tile).
 template <int D, int N>
@@ -441,7 +498,7 @@ __device__ __noinline__ void move_references(uint8_t* smem, uint32_t tmem, int c
   if (tid < kG) {
     const float* m4 = wm + c0 + tid;
     const float m = fmaxf(fmaxf(m4[0], m4[N]), fmaxf(m4[2 * N], m4[3 * N]));
-    const float old = nb[c0 + tid], now = m + old > kPTop ? kPLog2 - kHeadroom - m : old;
+    const float old = nb[c0 + tid], now = m + old > kPTop ? kPLog2 - m : old;
     nb[c0 + tid] = now;
     al[c0 + tid] = ex2_approx(now - old);
   }
@@ -457,8 +514,8 @@ __device__ __noinline__ void move_references(uint8_t* smem, uint32_t tmem, int c
     for (int k = 0; k < 8; ++k) any = any || f[k] != 1.f;
     if (!any) continue;
 #pragma unroll 1
-    for (int z = 0; z < 3; ++z) {  // O's two terms, row sums
-      const uint32_t at = at0 + (z < 2 ? C::kColO + (w * 2 + z) * N : C::kColL + w * N) + c;
+    for (int z = 0; z < 4; ++z) {  // O's three terms, row sums
+      const uint32_t at = at0 + (z < 3 ? C::kColO + (w * 3 + z) * N : C::kColL + w * N) + c;
       uint32_t o[8];
       tmem_get<8>(at, o);
 #pragma unroll
@@ -570,10 +627,10 @@ __device__ __forceinline__ int plan_segments(const Params& p, const Plan& plan, 
 // both, page by page into the ring. The scales go along as bytes, or (scales not
 // null) through registers and into shared memory as floats, with the keys that are
 // there as bits.
-template <class C>
+template <class C, class W>
 __device__ __forceinline__ void load_tiles(const Params& p, uint8_t* smem, const Seg* segs, int count, int g, bool is_v,
                                            uint64_t* full, uint64_t* empty, uint32_t* good, volatile int* issued,
-                                           Waiter& wait, bool elected, int lane, float* scales = nullptr,
+                                           W& wait, bool elected, int lane, float* scales = nullptr,
                                            uint32_t* lives = nullptr, uint64_t* c_full = nullptr,
                                            uint64_t* c_free = nullptr) {
   const int H = p.a.cache.H, ps = p.a.cache.page_size, ps_log = 31 - __clz(ps), ppt = 128 >> ps_log;
@@ -705,7 +762,7 @@ __device__ __forceinline__ void finish(const Params& p, int warp, bool elected, 
       // bounded drain of loads that were issued but never consumed
       for (int x = 0; x < 2; ++x) {
         uint64_t* full = x ? v_full : k_full;
-        for (int t = consumed[x]; t < issued[x]; ++t) {
+        for (int t = max(consumed[x], issued[x] - kStages); t < issued[x]; ++t) {  // (a stage loaded again was waited for)
           const unsigned long long t0 = globaltimer_ns();
           while (!mbar_try_wait(smem_u32(full + t % kStages), (t / kStages) & 1) && globaltimer_ns() - t0 < kWaitTimeoutNs) {
           }
@@ -727,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Seg* segs = reinterpret_cast<Seg*>(smem + C::kOffSeg);
   float* qmul = reinterpret_cast<float*>(smem + C::kOffF);  // [2][N]
-  float* nbias = reinterpret_cast<float*>(smem + C::kOffBias);  // [2][kPar][N]: 6 - reference maximum
+  float* nbias = reinterpret_cast<float*>(smem + C::kOffBias);  // [2][kPar][N]: kPLog2 - reference maximum
   float* lsum = reinterpret_cast<float*>(smem + C::kOffMax) + 4 * C::kPar * N;  // [2][kPar][4][N], behind wmax [kPar][4][N]
   float* fin = lsum + 8 * C::kPar * N;                      // [kPar + 1][N]: weights of the parities, 1 / l
   int* lim = reinterpret_cast<int*>(smem + C::kOffAlpha) + C::kPar * N;  // [2][N]: last key a row sees (without a tree)
@@ -797,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Waiter wait{abort_flag};
+  Waiter<true> wait{abort_flag};
   int seg0 = 0, nsegs = 0;
   int g = 0;  // tiles so far; every role counts the same ones
   // Segments are planned kSegs at a time (one pass unless the sequences are many and short).
@@ -811,7 +868,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
                     issued, wait, elected, lane);
     } else if (warp == 1) {
       // ---------------------------------------------------------- PV issuer
-      constexpr uint32_t kHi = idesc_f8(D, N, 0, 1, 1), kLo = idesc_f8(D, N, 1, 1, 1);
+      constexpr uint32_t kPV = idesc(D, 3 * N, 1, 1, 1);
       for (int i = 0, gg = g; i < count; ++i) {
         const int nt = segs[i].nt, sg = seg0 + i;
         if (sg > 0) wait.warp(epi, (sg - 1) & 1, kErrEpi);
@@ -824,14 +881,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
           const uint64_t v = make_smem_desc(smem_u32(smem + C::kOffV + st * C::kTile), 16, 8 * D, swz_of(D));
           const uint64_t pd =
               make_smem_desc(smem_u32(smem + C::kOffP + w * C::kPTile), 16, 8 * C::kPP, swz_of(C::kPP));
-          const uint32_t o = tmem + C::kColO + w * 2 * N;
+          const uint32_t o = tmem + C::kColO + w * 3 * N;
           if (elected) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_f8f6f4_ss(o + t * N, v + ((kk * 32 * D) >> 4), pd + ((t * C::kPLo + kk * 32 * C::kPP) >> 4),
-                              t ? kLo : kHi, (j >= C::kPar || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f8f6f4_ss(o, v + ((kk * 32 * D) >> 4), pd + ((kk * 32 * C::kPP) >> 4), kPV,
+                            (j >= C::kPar || kk > 0) ? 1u : 0u);
             mma_commit(v_empty + st);
             mma_commit(o_done + w);
             consumed[1] = gg + 1;
@@ -841,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
       }
     } else if (warp == 2) {
       // ----------------------------------------------------------- S issuer
-      constexpr uint32_t kS = idesc_f8(128, N, 0, 0, 0);
+      constexpr uint32_t kS = idesc(128, N, 0, 0);
       for (int i = 0, gg = g; i < count; ++i) {
         const int nt = segs[i].nt, sg = seg0 + i;
         wait.warp(q_full + (sg & 1), (sg >> 1) & 1, kErrQFull);
@@ -1017,7 +1072,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
             }
             if (!idle) wait.warp(o_done + w, (it - 1) & 1, kErrODone);
             idle = true;
-            uint32_t hi[kG / 4], lo[kG / 4];
+            uint32_t hi[kG / 4], mid[kG / 4], lo[kG / 4];
 #pragma unroll
             for (int c = 0; c < kG; c += 4) {
               float q[4];
@@ -1029,16 +1084,15 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
                 q[2 * k + 1] = ex2_approx(b);
                 x[c / 2 + k] = f2_pack(q[2 * k], q[2 * k + 1]);
               }
-              split_p(q[0], q[1], q[2], q[3], hi[c / 4], lo[c / 4]);
+              split_p(q[0], q[1], q[2], q[3], hi[c / 4], mid[c / 4], lo[c / 4]);
             }
             const uint32_t at = tid * C::kPP + c0;
-            if (kG == 8) {
-              *reinterpret_cast<uint2*>(p_tile + swizzled<C::kPP>(at)) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(p_tile + swizzled<C::kPP>(at + C::kPLo)) = make_uint2(lo[0], lo[1]);
-            } else {
-              *reinterpret_cast<uint4*>(p_tile + swizzled<C::kPP>(at)) = make_uint4(hi[0], hi[1], hi[kG / 4 - 2], hi[kG / 4 - 1]);
-              *reinterpret_cast<uint4*>(p_tile + swizzled<C::kPP>(at + C::kPLo)) =
-                  make_uint4(lo[0], lo[1], lo[kG / 4 - 2], lo[kG / 4 - 1]);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) {
+              const uint32_t* t = z == 0 ? hi : (z == 1 ? mid : lo);
+              uint8_t* dst = p_tile + swizzled<C::kPP>(at + z * N);
+              if (kG == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(t[0], t[1]);
+              else *reinterpret_cast<uint4*>(dst) = make_uint4(t[0], t[1], t[kG / 4 - 2], t[kG / 4 - 1]);
             }
             uint32_t l[kG];
             tmem_get<kG>(t_l + c0, l);
@@ -1144,14 +1198,20 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
 #pragma unroll 1
           for (int x = 0; x < C::kPar; ++x) {
             if (!(had >> x & 1u)) continue;
-            uint32_t hi[8], lo[8];
-            tmem_ld8(t_o + x * 2 * N + c0, hi);
-            tmem_ld8(t_o + x * 2 * N + N + c0, lo);
+            uint32_t hi[8], mid[8], lo[8];
+            const uint32_t at = t_o + x * 3 * N + c0;
+            tmem_ld8(at, hi);
+            tmem_ld8(at + N, mid);
+            tmem_ld8(at + 2 * N, lo);
             tmem_wait8(hi);
+            tmem_wait8(mid);
             tmem_wait8(lo);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              o[k] = fmaf(fin[x * N + c0 + k], fmaf(__uint_as_float(lo[k]), 1.f / kLoScale, __uint_as_float(hi[k])), o[k]);
+              o[k] = fmaf(fin[x * N + c0 + k],
+                          fmaf(__uint_as_float(lo[k]), 1.f / kLoScale,
+                               fmaf(__uint_as_float(mid[k]), 1.f / kMidScale, __uint_as_float(hi[k]))),
+                          o[k]);
           }
           int t = (s.rt * N + c0) / p.group, hg = s.rt * N + c0 - t * p.group;
 #pragma unroll
@@ -1190,20 +1250,22 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
 // core's 128 rows, so that a row's maximum and sum stay with one thread a half of
 // the keys and nothing is agreed on between warps. The softmax bounds it: 16384
 // exponentials a tile are 1024 cycles of the special-function units and the
-// products 1024 of the tensor core (d = 128), a tile takes 3000: two softmax warps
-// a scheduler, whose 750 instructions a tile issue at 0.43 a cycle, so that the
-// latencies show (leaving out any one part of the softmax gains 3 to 8%). A tree of
-// 61 tokens, group 4, on 8 sequences of up to 16384: 163 us, 0.29 of the measured
-// bf16 rate; 3 chunks of up to 1024 queries at up to 16384 tokens, d = 64: 478 us.
-// Measured against it on the chunks: 16 warps with two threads a row 531 us; one S,
-// P beside it 510 (503 then); each half of the keys with its own S products 522;
-// the exponentials of 32 keys beside the scores of the next 32 709.
-//   Q in two E4M3 terms as above; K and V as they are; the scales of keys are
+// products 1024 of the tensor core (d = 128), and two softmax warps a scheduler do not
+// cover their latencies. A tree of 61 tokens, group 4, on 8 sequences of up to 16384:
+// 158 us, 0.30 of the measured bf16 rate; 3 chunks of up to 1024 queries at up to 16384
+// tokens, d = 64: 451 us, d = 128: 491 us.
+// Measured against it on the chunks (d = 64; P was two 8-bit terms then): 16 warps with
+// two threads a row 531 us against 503; one S, P beside it 510; each half of the keys with
+// its own S products 522; the exponentials of 32 keys beside the scores of the next 32 709.
+//   Q in two E4M3 terms as above, K as it is; the scales of keys are
 //   per column here: a loading warp writes 2^ek, ev and 2^-ev of a tile's keys to
 //   shared memory
-//   P = Phi + Plo in tensor memory, E4M3 and E5M2 at one scale (one O): 2^-7 of
-//   each value down to 2^-16 of the largest, 3 bits of it to 2^-20, a floor near 2^-23
-// CTA (persistent, 384 threads): warps 0, 3 load, 1 issues P V, 2 issues Q K^T,
+//   P in fp16 in tensor memory, and V as fp16 copies of its codes, which are exact, in
+//   shared memory: P 2^ev is 2^10 or more for the row's largest, 11 bits down to 2^-24 of
+//   that, an error of at most 2^-35 of it below. (In three E5M2 terms as above the splitting
+//   would be twice the softmax's conversions.) Four warps make the copies: made by the softmax
+//   warps, chunks and tree took 500, 544 and 172 us
+// CTA (persistent, 512 threads): warps 0, 3 load, 1 issues P V, 2 issues Q K^T, 12-15 widen V,
 // 4-11 softmax: warp 4 + 4 h + q has rows 32 q .. + 31 and keys 64 h .. + 63 of every
 // tile, a thread a row, with its own reference maxima, sums and O, so that no lane
 // waits on another and all lanes of a warp read the same scales; the halves are
@@ -1213,16 +1275,22 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
 // ---------------------------------------------------------------------------
 template <int D>
 struct Wide {
-  static constexpr int kD = D, kThreads = 384, N = 128;
+  static constexpr int kD = D, kThreads = 512, N = 128;
+  // Registers a thread, 128 at launch: four warps that load and issue, four that widen V, eight of softmax. The chunks at
+  // d = 128 take 491 us so, 518 with 88, 56 and 184, 540 with 112, 48 and 176, 511 with 104, 72 and 168.
+  static constexpr int kRegsHelp = 96, kRegsWiden = 64, kRegsSoftmax = 176;
+  static_assert(kRegsHelp + kRegsWiden + 2 * kRegsSoftmax <= 4 * 128, "registers");
   static constexpr int kTile = 128 * D, kQ = 128 * D;
   static constexpr int kScl = 4;                         // tiles of scales in flight
   static constexpr int kWords = kScl * (3 * 128 + 4) + 2 * 128 + 2 * 128 + 2 * 2 * 128;  // see the kernel
-  static constexpr int kFixed = 4 * kQ + 4 * kWords + kSegs * static_cast<int>(sizeof(Seg)) + 1024;
+  static constexpr int kWide = 2 * kTile;                // bytes of a V tile in fp16
+  static constexpr int kFixed = 4 * kQ + 2 * kWide + 4 * kWords + kSegs * static_cast<int>(sizeof(Seg)) + 1024;
   static constexpr int kRoom = (227 * 1024 - 1024 - kFixed) / (2 * kTile);
   static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
   static constexpr int kOffK = 0, kOffV = kOffK + kStages * kTile;
   static constexpr int kOffQ = kOffV + kStages * kTile;  // [2 buffers][2 terms][128][D]
-  static constexpr int kOffSeg = kOffQ + 4 * kQ;
+  static constexpr int kOffW = kOffQ + 4 * kQ;           // [2]: V in fp16
+  static constexpr int kOffSeg = kOffW + 2 * kWide;
   static constexpr int kOffF = kOffSeg + kSegs * static_cast<int>(sizeof(Seg));
   static constexpr int kOffBar = (kOffF + 4 * kWords + 7) & ~7;
   static constexpr int kBars = 4 * kStages + 2 * 3 + 2 + 1 + 2 + 2 * kScl;
@@ -1230,31 +1298,10 @@ struct Wide {
   static constexpr int kOffScan = kOffMisc + 64;
   static constexpr int kBytes = kOffScan + 2 * 32 * 4;
   static constexpr int kSmem = kBytes + 1024;
-  static_assert(kSmem <= 227 * 1024 && kStages >= 3 && kOffF % 16 == 0, "shared memory");
+  static_assert(kSmem <= 227 * 1024 && kStages >= 2 && kOffF % 16 == 0, "shared memory");
   static constexpr int kOffE = 0;                        // (no ring of scale bytes)
   static constexpr int kColS = 0, kColO = 256;           // S [2][128], O [2 key halves][D at 128 each]
 };
-
-// Four P as E4M3 codes, and what they leave as E5M2 codes at the same scale.
-__device__ __forceinline__ void split_p1(float p0, float p1, float p2, float p3, uint32_t& hi, uint32_t& lo) {
-  asm("{\n\t"
-      ".reg .b16 a, b, c, d;\n\t"
-      ".reg .b32 h0, h1, r0, r1;\n\t"
-      "cvt.rn.f16x2.f32 h0, %3, %2;\n\t"
-      "cvt.rn.f16x2.f32 h1, %5, %4;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 a, h0;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 b, h1;\n\t"
-      "mov.b32 %0, {a, b};\n\t"
-      "cvt.rn.f16x2.e4m3x2 r0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 r1, b;\n\t"
-      "sub.rn.f16x2 r0, h0, r0;\n\t"
-      "sub.rn.f16x2 r1, h1, r1;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 c, r0;\n\t"
-      "cvt.rn.satfinite.e5m2x2.f16x2 d, r1;\n\t"
-      "mov.b32 %1, {c, d};\n\t}"
-      : "=r"(hi), "=r"(lo)
-      : "f"(p0), "f"(p1), "f"(p2), "f"(p3));
-}
 
 // Drafted tokens first + d .. first + d + 31 of a tree's row as bits (d < 0: the tokens before them, all seen).
 __device__ __forceinline__ uint32_t tree_bits(const long long* words, int n_words, int d) {
@@ -1281,7 +1328,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
   uint64_t* k_full = bars;                // [stage]
   uint64_t* v_full = k_full + kStages;    // [stage]
   uint64_t* k_empty = v_full + kStages;   // [stage]
-  uint64_t* v_empty = k_empty + kStages;  // [stage]
+  uint64_t* v_empty = k_empty + kStages;  // [stage]: widened to fp16
   uint64_t* s_full = v_empty + kStages;   // [tile parity]: scores and scales, 2 arrivals
   uint64_t* p_full = s_full + 2;          // [tile parity], 8 arrivals
   uint64_t* o_done = p_full + 2;          // [tile parity]
@@ -1289,7 +1336,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
   uint64_t* epi = q_full + 2;             // 8 arrivals
   uint64_t* drain = epi + 1;              // [2]
   uint64_t* c_full = drain + 2;           // [kScl]: a tile's scales are written
-  uint64_t* c_free = c_full + C::kScl;    // [kScl], 8 arrivals: and were read
+  uint64_t* c_free = c_full + C::kScl;    // [kScl], 9 arrivals: and were read
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* issued = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
@@ -1306,17 +1353,17 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
       mbar_init(k_full + s, 1);
       mbar_init(v_full + s, 1);
       mbar_init(k_empty + s, 1);
-      mbar_init(v_empty + s, 1);
+      mbar_init(v_empty + s, 4);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 2);
-      mbar_init(p_full + w, 8);
+      mbar_init(p_full + w, 12);
       mbar_init(o_done + w, 1);
       mbar_init(q_full + w, 8);
       mbar_init(drain + w, 1);
     }
     mbar_init(epi, 8);
-    for (int s = 0; s < C::kScl; ++s) mbar_init(c_full + s, 1), mbar_init(c_free + s, 8);
+    for (int s = 0; s < C::kScl; ++s) mbar_init(c_full + s, 1), mbar_init(c_free + s, 12);
     *abort_flag = 0;
     issued[0] = issued[1] = consumed[0] = consumed[1] = 0;
     *has_tail = 0;
@@ -1336,80 +1383,116 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  Waiter wait{abort_flag};
+  Waiter<false> wait{abort_flag};
   int seg0 = 0, nsegs = 0;
   int g = 0;
-  do {
+  // The next batch of segments; every role plans with the block and then counts the same tiles.
+  auto next = [&]() {
     __syncthreads();
     nsegs = plan_segments<N>(p, plan, seg0, segs, first_seg, last_seg, has_tail);
-    const int count = min(kSegs, nsegs - seg0);
-    if (warp == 0 || warp == 3) {
-      load_tiles<C>(p, smem, segs, count, g, warp != 0, warp != 0 ? v_full : k_full, warp != 0 ? v_empty : k_empty,
-                    nullptr, issued, wait, elected, lane, scales, lives, c_full, c_free);
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- PV issuer
-      constexpr uint32_t kHi = idesc_f8(128, D, 0, 0, 1, 0), kLo = idesc_f8(128, D, 0, 0, 1, 1);
-      for (int i = 0, gg = g; i < count; ++i) {
-        const int nt = segs[i].nt, sg = seg0 + i;
-        if (sg > 0) wait.warp(epi, (sg - 1) & 1, kErrEpi);
-        for (int j = 0; j < nt; ++j, ++gg) {
-          const int st = gg % kStages, w = gg & 1;
-          bool ok = wait.warp(p_full + w, (gg >> 1) & 1, kErrPFull);
-          ok = wait.warp(v_full + st, (gg / kStages) & 1, kErrVFull) && ok;
-          if (!ok) continue;
-          tc_fence_after();
-          const uint64_t v = make_smem_desc(smem_u32(smem + C::kOffV + st * C::kTile), 16, 8 * D, swz_of(D));
-          const uint32_t pt = tmem + C::kColS + w * 128;
-          if (elected) {
+    return min(kSegs, nsegs - seg0);
+  };
+  auto more = [&](int count) {
+    for (int i = 0; i < count; ++i) g += segs[i].nt;
+    seg0 += kSegs;
+    return seg0 < nsegs;
+  };
+  if (warp < 4) {
+    reg_dealloc<C::kRegsHelp>();
+    int count;
+    do {
+      count = next();
+      if (warp == 0 || warp == 3) {
+        load_tiles<C>(p, smem, segs, count, g, warp != 0, warp != 0 ? v_full : k_full, warp != 0 ? v_empty : k_empty,
+                      nullptr, issued, wait, elected, lane, scales, lives, c_full, c_free);
+      } else if (warp == 1) {
+        // ---------------------------------------------------------- PV issuer
+        constexpr uint32_t kPV = idesc(128, D, 0, 1);
+        for (int i = 0, gg = g; i < count; ++i) {
+          const int nt = segs[i].nt, sg = seg0 + i;
+          for (int j = 0; j < nt; ++j, ++gg) {
+            const int w = gg & 1;
+            if (j == 0 && sg > 0) wait.warp(epi, (sg - 1) & 1, kErrEpi);
+            if (!wait.warp(p_full + w, (gg >> 1) & 1, kErrPFull)) continue;
+            tc_fence_after();
+            // 64 channels of a key are 128 bytes; the next 64 lie a whole tile of keys on
+            const uint64_t v = make_smem_desc(smem_u32(smem + C::kOffW + w * C::kWide), 128 * 128, 8 * 128, swz_of(128));
+            const uint32_t pt = tmem + C::kColS + w * 128;
+            if (elected) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_f16_ts(tmem + C::kColO + h * 128, pt + h * 64 + 8 * kk, v + (((4 * h + kk) * 16 * 128) >> 4), kPV,
+                             (j > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(o_done + w);
+              consumed[1] = gg + 1;
+            }
+            __syncwarp();
+          }
+        }
+      } else {
+        // ----------------------------------------------------------- S issuer
+        constexpr uint32_t kS = idesc(128, 128, 0, 0);
+        for (int i = 0, gg = g; i < count; ++i) {
+          const int nt = segs[i].nt, sg = seg0 + i;
+          wait.warp(q_full + (sg & 1), (sg >> 1) & 1, kErrQFull);
+          tc_fence_after();
+          const uint64_t q = make_smem_desc(smem_u32(smem + C::kOffQ + (sg & 1) * 2 * C::kQ), 16, 8 * D, swz_of(D));
+          for (int j = 0; j < nt; ++j, ++gg) {
+            const int st = gg % kStages, w = gg & 1;
+            bool ok = wait.warp(k_full + st, (gg / kStages) & 1, kErrKFull);
+            if (gg >= 2) ok = wait.warp(o_done + w, ((gg >> 1) - 1) & 1, kErrODone) && ok;  // P lay in this S
+            ok = wait.warp(c_full + gg % C::kScl, (gg / C::kScl) & 1, kErrScales) && ok;    // so that one wait does for both
+            if (!ok) continue;
+            tc_fence_after();
+            const uint64_t k = make_smem_desc(smem_u32(smem + C::kOffK + st * C::kTile), 16, 8 * D, swz_of(D));
+            const uint32_t s = tmem + C::kColS + w * 128;
+            if (elected) {
 #pragma unroll
               for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
-                  mma_f8f6f4_ts(tmem + C::kColO + h * 128, pt + h * 64 + t * 16 + 8 * kk,
-                                v + (((2 * h + kk) * 32 * D) >> 4), t ? kLo : kHi, (j > 0 || t + kk > 0) ? 1u : 0u);
-            mma_commit(v_empty + st);
-            mma_commit(o_done + w);
-            consumed[1] = gg + 1;
+                for (int kk = 0; kk < D / 32; ++kk)
+                  mma_f8f6f4_ss(s, q + (C::kQ >> 4) * t + 2 * kk, k + 2 * kk, kS, t + kk > 0 ? 1u : 0u);
+              mma_commit(s_full + w);
+              mbar_arrive(s_full + w);
+              mma_commit(k_empty + st);
+              consumed[0] = gg + 1;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
-    } else if (warp == 2) {
-      // ----------------------------------------------------------- S issuer
-      constexpr uint32_t kS = idesc_f8(128, 128, 0, 0, 0);
-      for (int i = 0, gg = g; i < count; ++i) {
-        const int nt = segs[i].nt, sg = seg0 + i;
-        wait.warp(q_full + (sg & 1), (sg >> 1) & 1, kErrQFull);
-        tc_fence_after();
-        const uint64_t q = make_smem_desc(smem_u32(smem + C::kOffQ + (sg & 1) * 2 * C::kQ), 16, 8 * D, swz_of(D));
-        for (int j = 0; j < nt; ++j, ++gg) {
-          const int st = gg % kStages, w = gg & 1;
-          bool ok = wait.warp(k_full + st, (gg / kStages) & 1, kErrKFull);
-          if (gg >= 2) ok = wait.warp(o_done + w, ((gg >> 1) - 1) & 1, kErrODone) && ok;  // P lay in this S
-          ok = wait.warp(c_full + gg % C::kScl, (gg / C::kScl) & 1, kErrScales) && ok;    // so that one wait does for both
-          if (!ok) continue;
-          tc_fence_after();
-          const uint64_t k = make_smem_desc(smem_u32(smem + C::kOffK + st * C::kTile), 16, 8 * D, swz_of(D));
-          const uint32_t s = tmem + C::kColS + w * 128;
-          if (elected) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int kk = 0; kk < D / 32; ++kk)
-                mma_f8f6f4_ss(s, q + (C::kQ >> 4) * t + 2 * kk, k + 2 * kk, kS, t + kk > 0 ? 1u : 0u);
-            mma_commit(s_full + w);
-            mbar_arrive(s_full + w);
-            mma_commit(k_empty + st);
-            consumed[0] = gg + 1;
-          }
-          __syncwarp();
-        }
+    } while (more(count));
+  } else if (warp >= 12) {
+    // --------------------------------------------------------------- V to fp16
+    reg_dealloc<C::kRegsWiden>();
+    const int key = threadIdx.x & 127;
+    int count;
+    do {
+      count = next();
+      int tiles = 0;
+      for (int i = 0; i < count; ++i) tiles += segs[i].nt;
+      for (int gg = g; gg < g + tiles; ++gg) {
+        const int st = gg % kStages, sc = gg % C::kScl, w = gg & 1;
+        wait.warp(v_full + st, (gg / kStages) & 1, kErrVFull);
+        wait.warp(c_full + sc, (gg / C::kScl) & 1, kErrScales);
+        if (gg >= 2) wait.warp(o_done + w, ((gg >> 1) - 1) & 1, kErrODone);  // the copy's last product
+        widen_row<D, D / 16>(smem + C::kOffV + st * C::kTile, smem + C::kOffW + w * C::kWide, key, 0,
+                             lives[sc * 4 + (key >> 5)] >> lane & 1u);
+        fence_proxy_async_shared();
+        warp_arrive(v_empty + st);
+        warp_arrive(c_free + sc);
+        warp_arrive(p_full + w);
       }
-    } else {
+    } while (more(count));
+  } else {
+    reg_alloc<C::kRegsSoftmax>();
+    int count;
+    do {
+      count = next();
       // ------------------------------------------------------------ softmax
-      const int h = (warp - 4) >> 2, q4 = warp & 3, tid = threadIdx.x - 128;
+      const int h = (warp - 4) >> 2, q4 = warp & 3;
       const int row = q4 * 32 + lane;  // of the tile
       const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
       uint8_t* q_buf = smem + C::kOffQ;
@@ -1434,7 +1517,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
           words = p.a.tree + (p.a.q_start ? static_cast<long long>(s.row0 + t) * p.a.tree_words
                                           : s.b * p.a.tree_sb + static_cast<long long>(t) * p.a.tree_words);
         }
-        float nb = 0.f;      // 6 - reference maximum of the row, 0 while no key was seen
+        float nb = 0.f;      // 10 - reference maximum of the row, 0 while no key was seen
         bool fresh = true;   // no key was seen
         uint64_t sum[2] = {0ull, 0ull};
         const int g_end = gg + s.nt;
@@ -1498,7 +1581,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
           if (__any_sync(0xffffffffu, top > kPTop || (fresh && top > -INFINITY))) {
             // some row's score passed its reference, or is its first: see move_references
             const bool moves = top > kPTop || (fresh && top > -INFINITY);
-            const float now = moves ? nb + (kPLog2 - kWideHeadroom - top) : nb;
+            const float now = moves ? nb + (kPLog2 - top) : nb;
             const float factor = moves && !fresh ? ex2_approx(now - nb) : 1.f;
             const uint64_t d2 = f2_pack(now - nb, now - nb), f2 = f2_pack(factor, factor);
 #pragma unroll
@@ -1525,7 +1608,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
           // over the scores that this warp has read
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            uint32_t hi[8], lo[8];
+            uint32_t w[16];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const ulonglong2 c = iv[8 * y + k];
@@ -1535,24 +1618,11 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
               a0 = ex2_approx(a0), a1 = ex2_approx(a1), a2 = ex2_approx(a2), a3 = ex2_approx(a3);
               sum[0] = f2_fma(f2_pack(a0, a1), c.x, sum[0]);
               sum[1] = f2_fma(f2_pack(a2, a3), c.y, sum[1]);
-              split_p1(a0, a1, a2, a3, hi[k], lo[k]);
+              w[2 * k] = half_p(a0, a1), w[2 * k + 1] = half_p(a2, a3);
             }
-            tmem_st8(t_s + 8 * y, hi);
-            tmem_st8(t_s + 16 + 8 * y, lo);
+            tmem_st16(t_s + 16 * y, w);
           }
           warp_arrive(c_free + sc);
-          if (!full && tid < 128) {
-            // rows of V that nobody may see can hold NaN codes, and 0 * NaN would reach O
-            const int st = gg % kStages;
-            const uint32_t word = tid < 64 ? (tid < 32 ? lv.x : lv.y) : (tid < 96 ? lv.z : lv.w);
-            wait.warp(v_full + st, (gg / kStages) & 1, kErrVFull);
-            if (!(word >> (tid & 31) & 1u)) {
-              uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + st * C::kTile + tid * D);
-#pragma unroll 1
-              for (int k = 0; k < D / 16; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_shared();
-          }
           tmem_wait_st();
           tc_fence_before();
           warp_arrive(p_full + sb);
@@ -1614,10 +1684,8 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
         tc_fence_before();
         warp_arrive(epi);
       }
-    }
-    for (int i = 0; i < count; ++i) g += segs[i].nt;
-    seg0 += kSegs;
-  } while (seg0 < nsegs);
+    } while (more(count));
+  }
 
   finish<kStages>(p, warp, elected, drain, abort_flag, has_tail, issued, consumed, k_full, v_full);
   if (warp == 1) {
