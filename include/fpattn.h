@@ -629,8 +629,8 @@ typedef struct {
  * rounded after it was multiplied by the power of two of its V row, e: to 2^-9
  * of its value where a KV head has at most 32 query rows (max_queries * Hq / H),
  * to 2^-11 where it has more, down to 2^-24 of the row's largest p e; below, a
- * p e is off by at most 2^-33 (2^-35) of that. Sums, the row sum among them
- * (of P before it was rounded), in fp32.
+ * p e is off by at most 2^-33 (2^-35) of that. Scores, and sums, the row sum
+ * among them (of P before it was rounded), in fp32.
  * A page of the table outside the cache, and a length beyond the table, count
  * as tokens that nobody sees. A query that sees no token gets out = 0 and
  * lse = -inf. A NaN row of the cache makes NaN the results of the queries that

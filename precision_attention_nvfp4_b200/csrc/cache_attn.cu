@@ -76,7 +76,7 @@ constexpr float kPLog2 = 10.f;
 constexpr float kPTop = 15.75f;
 // What P1 leaves is at most 2^12, what P2 leaves of that 2^8: scaled into E5M2's range, the terms reach further down.
 constexpr float kMidScale = 8.f, kLoScale = 128.f;
-constexpr float kNever = -1e30f;    // reference maximum before any key was seen
+constexpr float kNever = -3e38f;    // reference maximum before any key was seen: below every score
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -164,6 +164,18 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// What is to be added to a row's exponents instead of nb, so that the largest, now `top`, becomes kPLog2. (For scores of
+// 2^27 and more a step of the sum is as large as P's range: then one that does not carry P past its largest.)
+__device__ __forceinline__ float reference(float top, float nb) {
+  const float now = nb + (kPLog2 - top);
+  return top + (now - nb) > kPTop ? now - fabsf(now) * 1.1920929e-7f : now;
+}
+// Both no more than top; a NaN stays.
+__device__ __forceinline__ uint64_t at_most(uint64_t x, float top) {
+  float a, b;
+  f2_unpack(x, a, b);
+  return f2_pack(a > top ? top : a, b > top ? top : b);
 }
 // Barrier of `n` threads; every thread of them always takes part (see the loops).
 __device__ __forceinline__ void named_sync(int id, int n) {
@@ -1025,9 +1037,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
 #pragma unroll 1
           for (int c0 = lo_row; c0 < rows; c0 += C::kGroup) {
             constexpr int kG = C::kGroup;
-            uint64_t x[kG / 2];  // two rows each: the exponent of P (score, V's scale, reference maximum), then P
+            uint64_t x[kG / 2];  // two rows each: the exponent of P (score, reference maximum, V's scale), then P
 #pragma unroll 1
-            for (;;) {
+            for (bool moved = false;; moved = true) {
               uint32_t r[kG];
               tmem_get<kG>(t_s + c0, r);
 #pragma unroll
@@ -1037,7 +1049,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                   const uint64_t acc = f2_pack(__uint_as_float(r[c + 2 * k]), __uint_as_float(r[c + 2 * k + 1]));
-                  x[c / 2 + k] = f2_add(f2_fma(f2_mul(acc, k ? qv.y : qv.x), km2, ev2), k ? bv.y : bv.x);
+                  x[c / 2 + k] = f2_add(f2_fma(f2_mul(acc, k ? qv.y : qv.x), km2, k ? bv.y : bv.x), ev2);
                 }
               }
               if (masked) {
@@ -1051,6 +1063,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
                     x[c / 2 + k] = f2_pack(((k ? m.z : m.x) & bit) ? a : -INFINITY, ((k ? m.w : m.y) & bit) ? b : -INFINITY);
                   }
                 }
+              }
+              if (moved) {
+                // (the steps of scores of 2^27 and more can carry P past its largest even so)
+#pragma unroll
+                for (int c = 0; c < kG / 2; ++c) x[c] = at_most(x[c], kPTop);
+                break;
               }
               float top = -INFINITY;
 #pragma unroll
@@ -1517,7 +1535,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
           words = p.a.tree + (p.a.q_start ? static_cast<long long>(s.row0 + t) * p.a.tree_words
                                           : s.b * p.a.tree_sb + static_cast<long long>(t) * p.a.tree_words);
         }
-        float nb = 0.f;      // 10 - reference maximum of the row, 0 while no key was seen
+        float nb = 0.f;      // kPLog2 - reference maximum of the row, 0 while no key was seen
         bool fresh = true;   // no key was seen
         uint64_t sum[2] = {0ull, 0ull};
         const int g_end = gg + s.nt;
@@ -1581,7 +1599,7 @@ __global__ void __launch_bounds__(Wide<D>::kThreads, 1) cache_attn_wide_kernel(c
           if (__any_sync(0xffffffffu, top > kPTop || (fresh && top > -INFINITY))) {
             // some row's score passed its reference, or is its first: see move_references
             const bool moves = top > kPTop || (fresh && top > -INFINITY);
-            const float now = moves ? nb + (kPLog2 - top) : nb;
+            const float now = moves ? reference(top, nb) : nb;
             const float factor = moves && !fresh ? ex2_approx(now - nb) : 1.f;
             const uint64_t d2 = f2_pack(now - nb, now - nb), f2 = f2_pack(factor, factor);
 #pragma unroll
