@@ -153,14 +153,29 @@ __device__ __forceinline__ float to_odd(double x) {
   const float f = __double2float_rz(x);
   return static_cast<double>(f) == x || !(fabsf(f) < INFINITY) ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
-// Where 3 bits of mantissa are kept: is the value within 2^-17 of the middle between two of them?
-__device__ __forceinline__ bool near_tie(float x) { return ((__float_as_uint(x) + 0x80040u) & 0xFFFFFu) < 0x80u; }
 // A rotated pair in 64 bits.
 __device__ __noinline__ float2 turned_pair(float x, float y, long long pos, unsigned long long turns, float m) {
   double s, c;
   sincos_turns(static_cast<unsigned long long>(pos), turns, m, s, c);
   const double a = x, b = y;
   return make_float2(to_odd(fma(a, c, -(b * s))), to_odd(fma(a, s, b * c)));
+}
+
+// Largest |f| of the row whose D / 16 threads call together, as an integer: its order is that of the floats, and a NaN is
+// above infinity.
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_amax(const float (&f)[16]) {
+  uint32_t a = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+  return a;
+}
+// The smallest e >= kMinExp with A <= 448 * 2^e = 1.75 * 2^(e + 8): a mantissa above .75 carries into the exponent.
+__device__ __forceinline__ int row_exp(uint32_t a) { return max(kMinExp, static_cast<int>((a + 0x1FFFFFu) >> 23) - 135); }
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return static_cast<uint32_t>(cvt_e4m3x2(a, b)) | static_cast<uint32_t>(cvt_e4m3x2(c, d)) << 16;
 }
 
 struct RotaryParams {
@@ -238,22 +253,27 @@ struct WriteParams {
   int* nonfinite;
 };
 
+enum : int { kPlain, kHalf, kInterleaved };  // is K rotated, and how
+
 // Row r of a token: K head r, V head r - H, Q head r - 2 H.
 // Bound by memory: 3 bytes a channel of K and V, 4 of Q; 15361 tokens of 8 KV and
-// 32 query heads, d = 128: 75 us, 4.6 TB/s; 68 without the second look at K's
-// values beside a rounding boundary, 93 with all of K's in 64 bits.
-template <int D>
-__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid_constant__ WriteParams p) {
+// 32 query heads, d = 128: 77 us, 4.5 TB/s; 68 without the second look at K's
+// values beside a rounding boundary, 93 with all of K's in 64 bits. Without
+// rotation (K and V alone) 22.7 us, 4.1 TB/s. The layout is a parameter of the
+// kernel: one kernel for all took 93 and 33 us (142 registers, 3 blocks an SM).
+template <int D, int kLayout>
+__global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const __grid_constant__ WriteParams p) {
   constexpr int kLanes = D / 16;
+  constexpr bool inter = kLayout == kInterleaved;
   griddep_wait();
   const int tok = blockIdx.x * (kCacheThreads / kLanes) + threadIdx.x / kLanes;
   // every thread stays for the shuffles below; a token past the end is read as the last one and written nowhere
   const bool live = tok < p.T;
   const long long t = live ? tok : p.T - 1;
   const int j = threadIdx.x % kLanes;
-  const Place pl = place_of<D>(j, p.tab.dim, p.tab.interleaved);
-  const bool turn = pl.ta || pl.tb;
-  const long long pos = p.tab.dim ? p.positions[t] : 0;
+  const Place pl = place_of<D>(j, p.tab.dim, inter);
+  const bool turn = kLayout != kPlain && (pl.ta || pl.tb);
+  const long long pos = kLayout != kPlain ? p.positions[t] : 0;
   const long long slot = p.slots[t];
   const int page_log = 31 - __clz(p.cache.page_size);
   const long long page = slot >> page_log;
@@ -282,7 +302,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
       float f[16];
       unpack(va[k], f);
       unpack(vb[k], f + 8);
-      if (turn && !is_v) turn_row(f, sn, cs, p.tab.interleaved);
+      if (turn && !is_v) turn_row(f, sn, cs, inter);
       if (is_q) {
         if (live) {
           uint4* o = p.q_out + t * p.ot + h * p.oh;
@@ -291,45 +311,63 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const __grid
         }
         continue;
       }
-      // the largest magnitude as an integer: its order is that of the floats, and a NaN is above infinity
-      uint32_t a = 0u;
+      uint32_t a = row_amax<kLanes>(f);
+      int e = row_exp(a);
+      float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e <= 120
+      uint32_t w[4];
+      if (kLayout != kPlain && !is_v) {  // (the same for the whole warp, as the votes below need)
+        // fp32 angles and products leave a pair off by less than 2^-21 (|x| + |y|) m, at most 2^-20 of its larger result.
+        // Pairs of which that decides a code (one element in 10000) are rotated again in 64 bits, and so is every pair
+        // of a row of whose exponent it decides (8 rows in a million).
+        const bool edge = a > 17u && row_exp(a - 17u) != row_exp(a + 17u);
+        const float off = up * 9.6e-7f;  // 2^-20, and a little for the rounding of what it is added to
+        float d[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) a = max(a, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i)
+          d[i] = (i < 4 ? pl.ta : pl.tb) ? off * fmaxf(fabsf(inter ? f[2 * i] : f[i]), fabsf(inter ? f[2 * i + 1] : f[8 + i])) : 0.f;
+        uint32_t differ[4];
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const bool bad = a >= 0x7F800000u;
-      // smallest e with A <= 448 * 2^e = 1.75 * 2^(e + 8): a mantissa above .75 carries into the exponent
-      const int e = max(kMinExp, static_cast<int>((a + 0x1FFFFFu) >> 23) - 135);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);  // 2^-e, e <= 120
-      if (turn && !is_v && !bad) {
-        // fp32 angles and products are off by some 2^-23, which beside a middle between two codes is a whole step: a
-        // pair that near (one element in 8192) is rotated again in 64 bits
-        uint32_t hit = 0u;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) hit |= near_tie(f[i]) ? 1u << i : 0u;
-        if (hit) {
+        for (int i = 0; i < 4; ++i) {
+          const float d0 = d[inter ? 2 * i : (4 * i) & 7], d1 = d[inter ? 2 * i : (4 * i + 1) & 7];
+          const float d2 = d[inter ? 2 * i + 1 : (4 * i + 2) & 7], d3 = d[inter ? 2 * i + 1 : (4 * i + 3) & 7];
+          const float* g = f + 4 * i;
+          w[i] = codes4(fmaf(g[0], up, d0), fmaf(g[1], up, d1), fmaf(g[2], up, d2), fmaf(g[3], up, d3));
+          differ[i] = w[i] ^ codes4(fmaf(g[0], up, -d0), fmaf(g[1], up, -d1), fmaf(g[2], up, -d2), fmaf(g[3], up, -d3));
+        }
+        if ((differ[0] | differ[1] | differ[2] | differ[3] | (edge ? 1u : 0u)) && a < 0x7F800000u) {
           float x[16];
           unpack(va[k], x);
           unpack(vb[k], x + 8);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int a0 = p.tab.interleaved ? 2 * i : i, a1 = p.tab.interleaved ? 2 * i + 1 : 8 + i;
-            if ((hit >> a0 | hit >> a1) & 1u && (i < 4 ? pl.ta : pl.tb)) {
-              const int pair = p.tab.interleaved ? 4 * (i < 4 ? pl.a : pl.b) + (i & 3) : 8 * j + i;
-              const float2 y = turned_pair(p.tab.interleaved ? x[2 * i] : x[i], p.tab.interleaved ? x[2 * i + 1] : x[8 + i], pos,
-                                           p.tab.turns[pair], p.tab.magnitude);
-              if (p.tab.interleaved) f[2 * i] = y.x, f[2 * i + 1] = y.y;
+            const uint32_t here = inter ? differ[i >> 1] >> (16 * (i & 1)) & 0xFFFFu
+                                        : (differ[i >> 2] | differ[2 + (i >> 2)]) >> (8 * (i & 3)) & 0xFFu;
+            if ((here || edge) && (i < 4 ? pl.ta : pl.tb)) {
+              const int pair = inter ? 4 * (i < 4 ? pl.a : pl.b) + (i & 3) : 8 * j + i;
+              const float2 y = turned_pair(inter ? x[2 * i] : x[i], inter ? x[2 * i + 1] : x[8 + i], pos, p.tab.turns[pair],
+                                           p.tab.magnitude);
+              if (inter) f[2 * i] = y.x, f[2 * i + 1] = y.y;
               else f[i] = y.x, f[8 + i] = y.y;
             }
           }
-        }
-      }
-      uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = bad ? 0u
-                   : static_cast<uint32_t>(cvt_e4m3x2(f[4 * i] * up, f[4 * i + 1] * up)) |
-                         static_cast<uint32_t>(cvt_e4m3x2(f[4 * i + 2] * up, f[4 * i + 3] * up)) << 16;
+          for (int i = 0; i < 4; ++i) w[i] = codes4(f[4 * i] * up, f[4 * i + 1] * up, f[4 * i + 2] * up, f[4 * i + 3] * up);
+        }
+        if (__any_sync(0xffffffffu, edge)) {
+          a = row_amax<kLanes>(f);
+          if (edge) {
+            e = row_exp(a);
+            up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = codes4(f[4 * i] * up, f[4 * i + 1] * up, f[4 * i + 2] * up, f[4 * i + 3] * up);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = codes4(f[4 * i] * up, f[4 * i + 1] * up, f[4 * i + 2] * up, f[4 * i + 3] * up);
+      }
+      const bool bad = a >= 0x7F800000u;
+      if (bad) w[0] = w[1] = w[2] = w[3] = 0u;
       if (store) {
         const long long row = page * p.H + h;
         uint8_t* codes = (is_v ? p.cache.v : p.cache.k) + ((row << page_log) + off) * D;
@@ -479,7 +517,12 @@ cudaError_t launch_cache_write(const KvCache& c, const Rows& k, const Rows& v, c
   const int lanes = c.d / 16, groups = kCacheThreads / lanes;
   p.per = rows_per_group(p.T, lanes, p.rows);
   const dim3 grid((p.T + groups - 1) / groups, (p.rows + p.per - 1) / p.per);
-  return launch_pdl(c.d == 128 ? cache_write_kernel<128> : cache_write_kernel<64>, grid, dim3(kCacheThreads), 0, st, p);
+  const int layout = tab.dim == 0 ? kPlain : (tab.interleaved ? kInterleaved : kHalf);
+  auto kernel = c.d == 128 ? (layout == kPlain ? cache_write_kernel<128, kPlain>
+                                               : (layout == kHalf ? cache_write_kernel<128, kHalf> : cache_write_kernel<128, kInterleaved>))
+                           : (layout == kPlain ? cache_write_kernel<64, kPlain>
+                                               : (layout == kHalf ? cache_write_kernel<64, kHalf> : cache_write_kernel<64, kInterleaved>));
+  return launch_pdl(kernel, grid, dim3(kCacheThreads), 0, st, p);
 }
 
 cudaError_t launch_cache_read(const KvCache& c, const long long* slots, const Rows& k, const Rows& v,
