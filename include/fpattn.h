@@ -514,7 +514,7 @@ typedef struct {
  *   WAVELENGTH  f_i k_i + f_i / factor (1 - k_i), k_i = clamp((n_i - slow) / (fast - slow), 0, 1),
  *               n_i = original_length f_i / (2 pi)
  * turns[i] receives f_i / (2 pi) (turns a position) as a 64-bit fixed-point
- * fraction: position * turns[i], in wrapping 64-bit arithmetic, is the angle
+ * fraction, off by at most two of its last place: position * turns[i], in wrapping 64-bit arithmetic, is the angle
  * with its whole turns gone, so the angle of a far position is as exact as
  * that of a near one. Errors: FPATTN_ERR_INVALID_ARG.
  */
@@ -540,8 +540,8 @@ typedef struct {
  * transpose != 0: by the transposed matrix, a' = m (a cos t + b sin t), b' = m (b cos t - a sin t): the
  * gradient with respect to x of a loss whose gradient with respect to the
  * result is given as x.
- * positions   device int64: [T], or [B, T] when positions_per_b != 0. Any value;
- *             angles are exact to 2^-33 turns for |position| < 2^31
+ * positions   device int64: [T], or [B, T] when positions_per_b != 0. Any value; an
+ *             angle is off by at most 2^-63 |position| turns (the table) and 2^-25 turns (fp32)
  * out         rows of x's shape; may be x itself (same data and strides), must
  *             not overlap it otherwise
  */

@@ -13,7 +13,7 @@
 //
 // Angles: the table holds the turns a position as 64-bit fractions, so
 // position * turns in wrapping integer arithmetic is the angle modulo a turn
-// exactly (to 2^-65 |position|), where fp32 angles lose 2^-24 |angle|. The
+// (to 2^-63 |position| turns), where fp32 angles lose 2^-24 |angle|. The
 // top 32 bits are split into a quadrant and a remainder within an eighth of a
 // turn, whose sine and cosine are Taylor sums (truncated below 3e-8).
 #include <cfloat>

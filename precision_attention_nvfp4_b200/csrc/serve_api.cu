@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr double kPi = 3.14159265358979323846;
+constexpr long double kPi = 3.14159265358979323846264338327950288L;
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -116,28 +116,30 @@ fpattn_status fpattn_rotary_turns(const fpattn_rotary_spec* spec, uint64_t* turn
                 std::isfinite(s.fast)))
     return FPATTN_ERR_INVALID_ARG;
   if (!(std::isfinite(s.magnitude) && s.magnitude >= 0.0)) return FPATTN_ERR_INVALID_ARG;
+  // long double has the 64 bits of mantissa that the turns have
+  using real = long double;
   const int half = s.dim / 2;
-  const double dim = s.dim;
-  const double base = s.scaling == FPATTN_ROTARY_NTK ? s.base * std::pow(s.factor, dim / (dim - 2.0)) : s.base;
-  double lo = 0.0, hi = 0.0;
+  const real dim = s.dim, factor = s.factor, slow = s.slow, fast = s.fast, length = s.original_length;
+  const real base = s.scaling == FPATTN_ROTARY_NTK ? s.base * std::pow(factor, dim / (dim - 2)) : static_cast<real>(s.base);
+  real lo = 0, hi = 0;
   if (s.scaling == FPATTN_ROTARY_YARN) {
-    auto at = [&](double t) { return dim * std::log(s.original_length / (2.0 * kPi * t)) / (2.0 * std::log(base)); };
-    lo = std::fmax(0.0, std::floor(at(s.fast)));
-    hi = std::fmin(dim - 1.0, std::ceil(at(s.slow)));
+    auto at = [&](real t) { return dim * std::log(length / (2 * kPi * t)) / (2 * std::log(base)); };
+    lo = std::fmax(real(0), std::floor(at(fast)));
+    hi = std::fmin(dim - 1, std::ceil(at(slow)));
   }
   for (int i = 0; i < half; ++i) {
-    double f = std::pow(base, -2.0 * i / dim);
+    real f = std::pow(base, -2 * i / dim);
     if (s.scaling == FPATTN_ROTARY_LINEAR) {
-      f /= s.factor;
+      f /= factor;
     } else if (s.scaling == FPATTN_ROTARY_YARN) {
-      const double r = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 1e-3)));
-      f = f * (1.0 - r) + f / s.factor * r;
+      const real r = std::fmin(real(1), std::fmax(real(0), (i - lo) / std::fmax(hi - lo, static_cast<real>(1e-3))));
+      f = f * (1 - r) + f / factor * r;
     } else if (s.scaling == FPATTN_ROTARY_WAVELENGTH) {
-      const double n = s.original_length * f / (2.0 * kPi);
-      const double k = std::fmin(1.0, std::fmax(0.0, (n - s.slow) / (s.fast - s.slow)));
-      f = f * k + f / s.factor * (1.0 - k);
+      const real n = length * f / (2 * kPi);
+      const real k = std::fmin(real(1), std::fmax(real(0), (n - slow) / (fast - slow)));
+      f = f * k + f / factor * (1 - k);
     }
-    turns[i] = static_cast<uint64_t>(std::ldexp(f / (2.0 * kPi), 64));  // f <= 1: below 2^62
+    turns[i] = static_cast<uint64_t>(std::rint(std::ldexp(f / (2 * kPi), 64)));  // f <= 1: below 2^62
   }
   *magnitude = static_cast<float>(
       s.magnitude > 0.0 ? s.magnitude : (s.scaling == FPATTN_ROTARY_YARN ? 0.1 * std::log(s.factor) + 1.0 : 1.0));
