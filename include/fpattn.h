@@ -562,7 +562,7 @@ typedef struct {
   uint8_t* v_codes; /* [num_pages, H, page_size, d] */
   uint8_t* exps;    /* [num_pages, H, 2, page_size]: [0] of K, [1] of V */
   int32_t num_pages;
-  int32_t H;         /* KV heads, at most 65535 */
+  int32_t H;         /* KV heads, at most 4096; num_pages * H below 2^31 */
   int32_t page_size; /* 16, 32, 64 or 128 tokens */
   int32_t d;         /* 64 or 128 */
 } fpattn_kv_cache;
@@ -635,6 +635,9 @@ typedef struct {
  * as tokens that nobody sees. A query that sees no token gets out = 0 and
  * lse = -inf. A NaN row of the cache makes NaN the results of the queries that
  * see it, and no other.
+ * Limits (FPATTN_ERR_UNSUPPORTED beyond): 2^30 keys a table row (max_pages * page_size), 2^28 query
+ * rows a KV head and sequence, 2^24 sequences, and B * H * ceil(rows / tile) * (ceil(keys / 128) + start) <= 2^30 with
+ * rows = max_queries * Hq / H, tile 16, 32 or 128 (the first that holds them, 128 at most), start 8, or 6 for 128
  * out  bf16 [rows, Hq, d] contiguous, lse float [rows, Hq] or NULL (natural
  *      log): the rows of no sequence are left as they were
  * workspace  device, 256-byte aligned, fpattn_cache_attention_workspace()

@@ -1902,6 +1902,14 @@ cudaError_t launch_t(const CacheAttnArgs& a, const Sizes& z, cudaStream_t st) {
 
 }  // namespace
 
+double cache_attention_units(const CacheAttnArgs& a) {
+  const int N = rows_a_tile(a);
+  const long long rows = static_cast<long long>(a.Tmax) * (a.Hq / a.cache.H);
+  const long long keys = static_cast<long long>(a.max_pages) * a.cache.page_size;
+  const long long cost = N == 128 ? kSegCost<128> : kSegCost<16>;
+  return static_cast<double>(a.B) * a.cache.H * ((rows + N - 1) / N) * ((keys + 127) / 128 + cost);
+}
+
 size_t cache_attention_workspace(const CacheAttnArgs& a) { return sizes_of(a).bytes; }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st) {

@@ -71,12 +71,10 @@ fpattn_status check_queries(const fpattn_kv_cache* cache, const fpattn_cache_que
   if (!(q->softmax_scale >= 0.f && q->softmax_scale <= 1e30f)) return FPATTN_ERR_INVALID_ARG;
   if (!aligned(q->page_table, 4) || !aligned(q->lengths, 4) || !aligned(q->q_start, 4) || !aligned(q->tree_mask, 8))
     return FPATTN_ERR_ALIGNMENT;
-  // keys, rows and the tiles of the whole call are counted in 32 bits
+  // keys, rows and (below) the work of the whole call are counted in 32 bits
   const long long keys = static_cast<long long>(q->max_pages) * a->cache.page_size;
   const long long rows = static_cast<long long>(q->max_queries) * (r.H / a->cache.H);
   if (keys > (1ll << 30) || rows > (1ll << 28) || q->B > (1 << 24)) return FPATTN_ERR_UNSUPPORTED;
-  const double tiles = static_cast<double>(q->B) * a->cache.H * ((rows + 15) / 16) * ((keys + 127) / 128 + 8);
-  if (tiles > static_cast<double>(1ll << 30)) return FPATTN_ERR_UNSUPPORTED;
   a->q = r.data;
   a->q_sb = r.sb, a->q_st = r.st, a->q_sh = r.sh;
   a->q_start = q->q_start;
@@ -92,6 +90,7 @@ fpattn_status check_queries(const fpattn_kv_cache* cache, const fpattn_cache_que
   a->tree = reinterpret_cast<const long long*>(q->tree_mask);
   a->tree_words = q->tree_words;
   a->tree_sb = q->tree_stride_b;
+  if (fpattn::cache_attention_units(*a) > static_cast<double>(1ll << 30)) return FPATTN_ERR_UNSUPPORTED;
   a->scale = q->softmax_scale > 0.f ? q->softmax_scale : 1.0f / std::sqrt(static_cast<float>(a->cache.d));
   return FPATTN_OK;
 }

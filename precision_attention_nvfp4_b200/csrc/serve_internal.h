@@ -57,6 +57,8 @@ cudaError_t launch_cache_write(const KvCache& c, const Rows& k, const Rows& v, c
 cudaError_t launch_cache_read(const KvCache& c, const long long* slots, const Rows& k, const Rows& v,
                               cudaStream_t st);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t st);
+// The most units of work the launch above may plan (it counts them in 32 bits).
+double cache_attention_units(const CacheAttnArgs& a);
 // Bytes of device workspace the launch above needs for these sizes.
 size_t cache_attention_workspace(const CacheAttnArgs& a);
 // Error word of the cache attention's bounded waits.
