@@ -91,10 +91,49 @@ def _span(x: torch.Tensor) -> Tuple[int, int]:
     return a, a + (sum((n - 1) * st for n, st in zip(x.shape, x.stride())) + 1) * x.element_size()
 
 
+def _meet(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two tensors of one type and number of dimensions share an element: exactly where their strides agree
+    (heads of one projection lie between one another's), by their spans where they do not."""
+    if x.numel() == 0 or y.numel() == 0:
+        return False
+    (a, b), (c, d) = _span(x), _span(y)
+    if a >= d or c >= b:
+        return False
+    return _layouts_meet(c - a, x.element_size(), tuple(x.shape), x.stride(), tuple(y.shape), y.stride())
+
+
+@functools.lru_cache(maxsize=256)
+def _layouts_meet(distance, size, shape_x, strides_x, shape_y, strides_y) -> bool:
+    apart, odd = divmod(distance, size)
+    if odd:
+        return True
+    dims = []  # stride, and the least and the most of the difference of the two indices
+    for sx, sy, nx, ny in zip(strides_x, strides_y, shape_x, shape_y):
+        if nx > 1 and ny > 1 and sx != sy:
+            return True
+        if nx > 1 or ny > 1:
+            dims.append((sx if nx > 1 else sy, 1 - ny, nx - 1))
+    dims.sort(reverse=True)
+
+    def reach(left, i):  # is some index difference in dims[i:] worth `left` elements?
+        if i == len(dims):
+            return left == 0
+        stride, low, high = dims[i]
+        if stride == 0:
+            return reach(left, i + 1)
+        # what the dims after this one can make up for
+        down, up = (sum(dim[0] * dim[k] for dim in dims[i + 1:]) for k in (1, 2))
+        first, last = max(low, -((up - left) // stride)), min(high, (left - down) // stride)
+        return any(reach(left - z * stride, i + 1) for z in range(first, last + 1))
+
+    return reach(apart, 0)
+
+
 def _apart(x: torch.Tensor, y: torch.Tensor, name: str) -> None:
     """x may be y itself, but not reach into it otherwise."""
     if not (x.data_ptr() == y.data_ptr() and x.stride() == y.stride() and x.shape == y.shape):
-        _disjoint(x, y, name)
+        if _meet(x, y):
+            raise ValueError(f"{name}: overlaps an input")
 
 
 def _disjoint(x: torch.Tensor, y: torch.Tensor, name: str) -> None:
@@ -282,18 +321,18 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
         qr = _rows3(q, "q", dev)
         if q.shape[0] != T or q.shape[2] != d:
             raise ValueError("q: expected [T, heads, d] of k's T and d")
-        if q_out is None:
+        caller_q_out = q_out is not None
+        if not caller_q_out:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        else:
-            if not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape:
-                raise ValueError("q_out: expected a tensor of q's shape")
+        elif not isinstance(q_out, torch.Tensor) or q_out.shape != q.shape:
+            raise ValueError("q_out: expected a tensor of q's shape")
+        orow = _rows3(q_out, "q_out", dev)
+        if caller_q_out:
             _writable(q_out, "q_out")
             _apart(q_out, q, "q_out")
-            for x in (k, v):
-                # in place, q's heads may lie between those of k and v in one projection
-                if q_out.data_ptr() != q.data_ptr() or q.data_ptr() == x.data_ptr():
-                    _disjoint(q_out, x, "q_out")
-        orow = _rows3(q_out, "q_out", dev)
+            # (q's heads may lie between those of k and v in one projection)
+            if _meet(q_out, k) or _meet(q_out, v):
+                raise ValueError("q_out: overlaps k or v")
         if q.shape[1] == 0:
             qr = orow = None
     elif q_out is not None:
@@ -329,8 +368,8 @@ def cache_read(cache: KvCache, slots: torch.Tensor, *,
                 raise ValueError(f"{name}: expected [T, H, d] = {(T, H, d)}")
             _writable(t, name)
     kr, vr = _rows3(k, "out[0]", dev), _rows3(v, "out[1]", dev)
-    if out is not None and T > 0 and k.data_ptr() == v.data_ptr():
-        raise ValueError("out: the two tensors are the same")
+    if out is not None and _meet(k, v):
+        raise ValueError("out: the two tensors are the same memory, or share some")
     if T > 0:
         _launch(dev, "fpattn_cache_read", cache._c(), slot_p, kr, vr)
     return k, v
@@ -434,6 +473,10 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
     elif (not isinstance(lse, torch.Tensor) or lse.dtype != torch.float32 or lse.device != dev
           or lse.shape != q.shape[:-1] or not lse.is_contiguous()):
         raise ValueError(f"lse: expected a contiguous float32 tensor of q's shape without d on {dev}")
+    else:
+        _disjoint(lse, q, "lse")
+        if out.numel() > 0 and lse.numel() > 0 and _span(out)[0] < _span(lse)[1] and _span(lse)[0] < _span(out)[1]:
+            raise ValueError("out and lse overlap")
     if out.numel() == 0 or B == 0:
         return out, lse
     desc = _queries(*rows, start_p or 0, B, T, page_table.data_ptr(), page_table.shape[1], page_table.stride(0), len_p,
