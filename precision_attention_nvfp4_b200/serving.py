@@ -10,8 +10,8 @@
 
 As in the rest of the package every call marshals torch tensors into the C ABI
 and enqueues kernels on the current stream of the tensors' device. The results
-carry no autograd graph: inputs that require a gradient are refused while
-gradients are recorded.
+carry no autograd graph: tensors that require a gradient are refused while
+gradients are recorded, and dual tensors of forward mode.
 """
 from __future__ import annotations
 
@@ -21,6 +21,8 @@ import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
+
+from torch.autograd.forward_ad import unpack_dual as _unpack_dual
 
 from . import _lib
 
@@ -65,9 +67,16 @@ def _check_rows(x: torch.Tensor, name: str, sd: int, dev: Optional[torch.device]
         raise ValueError(f"{name}: expected CUDA bf16 rows with contiguous channels")
     if x.device != dev if dev is not None else not x.is_cuda:
         raise ValueError(f"{name}: expected a tensor on {dev or 'a CUDA device'}")
+    _no_graph(x, name)
+
+
+def _no_graph(x: torch.Tensor, name: str) -> None:
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: requires a gradient, but this call records no graph (detach it; the gradient of "
                          "rotary is rotary with transpose=True)")
+    if _unpack_dual(x).tangent is not None:
+        raise ValueError(f"{name}: carries a forward-mode tangent, which this call would drop (unpack it; rotary is "
+                         "linear: the tangent of its result is rotary of the tangent)")
 
 
 def _vector(x: torch.Tensor, name: str, n: int, dtype: torch.dtype, dev: torch.device) -> int:
@@ -466,6 +475,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
           or out.shape != q.shape or not out.is_contiguous()):
         raise ValueError(f"out: expected a contiguous bf16 tensor of q's shape on {dev}")
     else:
+        _no_graph(out, "out")
         _disjoint(out, q, "out")
     if lse is None:
         if return_lse:
@@ -474,6 +484,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
           or lse.shape != q.shape[:-1] or not lse.is_contiguous()):
         raise ValueError(f"lse: expected a contiguous float32 tensor of q's shape without d on {dev}")
     else:
+        _no_graph(lse, "lse")
         _disjoint(lse, q, "lse")
         if out.numel() > 0 and lse.numel() > 0 and _span(out)[0] < _span(lse)[1] and _span(lse)[0] < _span(out)[1]:
             raise ValueError("out and lse overlap")
