@@ -11,7 +11,8 @@
 As in the rest of the package every call marshals torch tensors into the C ABI
 and enqueues kernels on the current stream of the tensors' device. The results
 carry no autograd graph: tensors that require a gradient are refused while
-gradients are recorded, and dual tensors of forward mode.
+gradients are recorded, and dual tensors of forward mode. Caller's outputs
+(out, lse, q_out) count as written in place.
 """
 from __future__ import annotations
 
@@ -23,6 +24,7 @@ from typing import Optional, Sequence, Tuple
 import torch
 
 from torch.autograd.forward_ad import unpack_dual as _unpack_dual
+from torch.autograd.graph import increment_version as _written  # a caller's tensor was written in place
 
 from . import _lib
 
@@ -215,8 +217,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable, *, tran
     if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError("x: expected [T, H, d] or [B, H, N, d]")
     _check_rows(x, "x", x.stride(-1), None)
-    dev = x.device
-    if out is None:
+    dev, caller_out = x.device, out is not None
+    if not caller_out:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         if not isinstance(out, torch.Tensor) or out.shape != x.shape:
@@ -242,6 +244,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, table: RotaryTable, *, tran
     pos = _vector(positions, "positions", B * T if per_b else T, torch.int64, dev)
     if out.numel() > 0:
         _launch(dev, "fpattn_rotary", xr, table._c(dev), pos, 1 if per_b else 0, 1 if transpose else 0, orow)
+        if caller_out:
+            _written(out)
     return out
 
 
@@ -326,6 +330,7 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     elif positions is not None or q is not None:
         raise ValueError("positions and q go with a rotary table")
     qr = orow = None
+    caller_q_out = False
     if q is not None:
         qr = _rows3(q, "q", dev)
         if q.shape[0] != T or q.shape[2] != d:
@@ -351,6 +356,8 @@ def cache_write(cache: KvCache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
         flag_p = _vector(nonfinite_flag, "nonfinite_flag", 1, torch.int32, dev)
     if T > 0:
         _launch(dev, "fpattn_cache_write", cache._c(), kr, vr, slot_p, tab, pos_p, qr, orow, flag_p)
+        if caller_q_out:
+            _written(q_out)
     return q_out
 
 
@@ -381,6 +388,9 @@ def cache_read(cache: KvCache, slots: torch.Tensor, *,
         raise ValueError("out: the two tensors are the same memory, or share some")
     if T > 0:
         _launch(dev, "fpattn_cache_read", cache._c(), slot_p, kr, vr)
+        if out is not None:
+            _written(k)
+            _written(v)
     return k, v
 
 
@@ -469,6 +479,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
         elif lead != (T,):
             raise ValueError("tree_mask: expected [B, T, W] or [T, W]")
         tree_p = tree_mask.data_ptr()
+    written = []
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif (not isinstance(out, torch.Tensor) or out.dtype != torch.bfloat16 or out.device != dev
@@ -477,6 +488,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
     else:
         _no_graph(out, "out")
         _disjoint(out, q, "out")
+        written.append(out)
     if lse is None:
         if return_lse:
             lse = q.new_empty(q.shape[:-1], dtype=torch.float32)
@@ -485,6 +497,7 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
         raise ValueError(f"lse: expected a contiguous float32 tensor of q's shape without d on {dev}")
     else:
         _no_graph(lse, "lse")
+        written.append(lse)
         _disjoint(lse, q, "lse")
         if out.numel() > 0 and lse.numel() > 0 and _span(out)[0] < _span(lse)[1] and _span(lse)[0] < _span(out)[1]:
             raise ValueError("out and lse overlap")
@@ -497,6 +510,8 @@ def cache_attention(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, l
     ws = cache.exps.new_empty(need)
     _launch(dev, "fpattn_cache_attention", cache._c(), desc, out.data_ptr(), None if lse is None else lse.data_ptr(),
             ws.data_ptr(), need)
+    for x in written:
+        _written(x)
     return out, lse
 
 

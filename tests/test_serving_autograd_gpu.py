@@ -1,4 +1,4 @@
-"""The serving calls record no graph: they refuse what one would be lost for."""
+"""The serving calls record no graph: they refuse what one would be lost for, and say which caller's tensors they wrote."""
 import pytest
 import torch
 import torch.autograd.forward_ad as fwd
@@ -48,3 +48,18 @@ def test_a_forward_mode_tangent_is_refused():
             call(t)
             with pytest.raises(ValueError, match="tangent"):
                 call(fwd.make_dual(t, torch.ones_like(t)))
+
+
+def test_outputs_of_the_caller_count_as_written():
+    for name, t, call in calls():
+        before = t._version
+        call(t)
+        assert t._version == before + (1 if name in ("out", "out[0]", "out[1]", "q_out", "lse") else 0), name
+    cache, table, lengths = make([20], 2, D, 16, 1)
+    q = _q(5, 1, 3, 4, D)
+    out = torch.ones_like(q)
+    w = torch.ones(D, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = (out * w).sum()                                           # saves out
+    fp.cache_attention(q, cache, table, lengths, out=out)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
