@@ -475,7 +475,8 @@ fpattn_status fpattn_fwd_video(const fpattn_tensor* q, const fpattn_tensor* k, c
 /*
  * bf16 rows [B, T, H, d] with strides in elements between sequences, tokens
  * and heads; the d channels of a row are contiguous. data must be 16-byte
- * aligned and the strides multiples of 8 (FPATTN_ERR_ALIGNMENT otherwise).
+ * aligned and the strides multiples of 8 (FPATTN_ERR_ALIGNMENT otherwise); that
+ * of an axis of one element is not looked at.
  */
 typedef struct {
   void* data;

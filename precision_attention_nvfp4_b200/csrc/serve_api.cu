@@ -27,8 +27,10 @@ fpattn_status check_rows(const fpattn_rows* r, fpattn::Rows* out) {
   if (r->d != 64 && r->d != 128) return FPATTN_ERR_UNSUPPORTED;
   // heads are a grid's y index and tokens are counted in 32 bits
   if (r->H > 16384 || static_cast<long long>(r->B) * r->T > (1ll << 31) - 1) return FPATTN_ERR_UNSUPPORTED;
-  if (!aligned(r->data, 16) || ((r->stride_b | r->stride_t | r->stride_h) & 7)) return FPATTN_ERR_ALIGNMENT;
-  *out = fpattn::Rows{r->data, r->B, r->T, r->H, r->d, r->stride_b, r->stride_t, r->stride_h};
+  // the stride of an axis of one is never taken
+  const int64_t sb = r->B > 1 ? r->stride_b : 0, st = r->T > 1 ? r->stride_t : 0, sh = r->H > 1 ? r->stride_h : 0;
+  if (!aligned(r->data, 16) || ((sb | st | sh) & 7)) return FPATTN_ERR_ALIGNMENT;
+  *out = fpattn::Rows{r->data, r->B, r->T, r->H, r->d, sb, st, sh};
   return FPATTN_OK;
 }
 
