@@ -23,7 +23,7 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from torch.autograd.forward_ad import unpack_dual as _unpack_dual
+from torch.autograd import forward_ad as _forward_ad
 from torch.autograd.graph import increment_version as _written  # a caller's tensor was written in place
 
 from . import _lib
@@ -76,7 +76,8 @@ def _no_graph(x: torch.Tensor, name: str) -> None:
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name}: requires a gradient, but this call records no graph (detach it; the gradient of "
                          "rotary is rotary with transpose=True)")
-    if _unpack_dual(x).tangent is not None:
+    # (outside of a dual level, -1, there are no tangents: 1 us of a small call for its tensors)
+    if getattr(_forward_ad, "_current_level", 0) >= 0 and _forward_ad.unpack_dual(x).tangent is not None:
         raise ValueError(f"{name}: carries a forward-mode tangent, which this call would drop (unpack it; rotary is "
                          "linear: the tangent of its result is rotary of the tangent)")
 
