@@ -29,7 +29,9 @@ namespace {
 
 constexpr int kCacheThreads = 128;
 constexpr int kMinExp = -63;
-constexpr int kBatch = 4;  // rows a thread has in flight
+// Rows a thread has in flight: the prefill write takes 76.4 us with 4, 85.9 with 2, 76.8 with 8; the rotary gradient 26.1,
+// 29.3 and 26.1.
+constexpr int kBatch = 4;
 
 
 __device__ __forceinline__ float lo_bf16(uint32_t w) { return __uint_as_float(w << 16); }
@@ -192,7 +194,8 @@ struct RotaryParams {
 
 // A group of D / 16 threads takes one token and p.heads of its heads.
 // Bound by memory: 4 bytes a channel; 4 x 4096 tokens of 32 heads, d = 128: 43 us,
-// 6.2 TB/s; the transpose of 32 of 64 channels, 15003 tokens of 40 heads: 25.6 us, 6.0 TB/s.
+// 6.3 TB/s; the transpose of 32 of 64 channels, 15003 tokens of 40 heads: 27.6 us, 5.6 TB/s
+// (26.2 us in a replayed graph).
 template <int D>
 __global__ void __launch_bounds__(kCacheThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
   constexpr int kLanes = D / 16;
@@ -324,7 +327,9 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const __g
         float d[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          d[i] = (i < 4 ? pl.ta : pl.tb) ? off * fmaxf(fabsf(inter ? f[2 * i] : f[i]), fabsf(inter ? f[2 * i + 1] : f[8 + i])) : 0.f;
+          d[i] = (i < 4 ? pl.ta : pl.tb)
+                     ? off * fmaxf(fabsf(inter ? f[2 * i] : f[i]), fabsf(inter ? f[2 * i + 1] : f[8 + i]))
+                     : 0.f;
         uint32_t differ[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -359,7 +364,8 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const __g
             e = row_exp(a);
             up = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = codes4(f[4 * i] * up, f[4 * i + 1] * up, f[4 * i + 2] * up, f[4 * i + 3] * up);
+            for (int i = 0; i < 4; ++i)
+              w[i] = codes4(f[4 * i] * up, f[4 * i + 1] * up, f[4 * i + 2] * up, f[4 * i + 3] * up);
           }
         }
       } else {
@@ -383,7 +389,8 @@ __global__ void __launch_bounds__(kCacheThreads, 4) cache_write_kernel(const __g
   griddep_launch_dependents();
 }
 
-constexpr int kReadBatch = 8;  // 68 us against 70 with four (prefix of 65536 tokens, 8 heads, d = 128); a write with eight took 79 us against 68
+// 67.4 us in a replayed graph against 68.9 with four (prefix of 65536 tokens, 8 heads, d = 128).
+constexpr int kReadBatch = 8;
 
 struct ReadParams {
   uint4 *k, *v;
@@ -407,7 +414,8 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two, float scale) {
 }
 
 // Thread j of a row takes codes 16 j .. 16 j + 15.
-// Bound by memory: 3 bytes a channel; 65536 tokens of 8 heads, d = 128: 68 us, 5.9 TB/s.
+// Bound by memory: 3 bytes a channel; 65536 tokens of 8 heads, d = 128: 71.5 us, 5.6 TB/s
+// (67.4 us, 6.0 TB/s, in a replayed graph).
 template <int D>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int kLanes = D / 16;
@@ -463,6 +471,10 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const __grid_
 // Rows of a token that a group of threads takes: kRowsMost of them once there
 // are tokens enough (one set of angles serves them, and the last wave of short
 // blocks is a small part), fewer when there are not, so that the card is filled.
+// With 2, 4, 8, 16 and 32 at most the prefill write takes 107, 82, 76, 77 and 77 us, the
+// read of a prefix 106, 82, 67, 70 and 70. Threads to fill the card with, 148 times 512,
+// 1024, 2048 and 4096: the same for many tokens, a write of 1000 tokens 8.2, 7.7, 8.6
+// and 12.4 us, 15361 tokens of d = 64 40.0, 40.0, 40.3 and 46.6.
 constexpr int kRowsMost = 8;
 int rows_per_group(long long tokens, int lanes, int rows) {
   const long long want = 148ll * 2048;  // threads
@@ -517,11 +529,13 @@ cudaError_t launch_cache_write(const KvCache& c, const Rows& k, const Rows& v, c
   const int lanes = c.d / 16, groups = kCacheThreads / lanes;
   p.per = rows_per_group(p.T, lanes, p.rows);
   const dim3 grid((p.T + groups - 1) / groups, (p.rows + p.per - 1) / p.per);
-  const int layout = tab.dim == 0 ? kPlain : (tab.interleaved ? kInterleaved : kHalf);
-  auto kernel = c.d == 128 ? (layout == kPlain ? cache_write_kernel<128, kPlain>
-                                               : (layout == kHalf ? cache_write_kernel<128, kHalf> : cache_write_kernel<128, kInterleaved>))
-                           : (layout == kPlain ? cache_write_kernel<64, kPlain>
-                                               : (layout == kHalf ? cache_write_kernel<64, kHalf> : cache_write_kernel<64, kInterleaved>));
+  auto pick = [&](auto plain, auto half, auto interleaved) {
+    return tab.dim == 0 ? plain : (tab.interleaved ? interleaved : half);
+  };
+  auto kernel = c.d == 128 ? pick(cache_write_kernel<128, kPlain>, cache_write_kernel<128, kHalf>,
+                                  cache_write_kernel<128, kInterleaved>)
+                           : pick(cache_write_kernel<64, kPlain>, cache_write_kernel<64, kHalf>,
+                                  cache_write_kernel<64, kInterleaved>);
   return launch_pdl(kernel, grid, dim3(kCacheThreads), 0, st, p);
 }
 

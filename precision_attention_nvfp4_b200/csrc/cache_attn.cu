@@ -41,9 +41,11 @@
 // cut in several leaves unnormalised partial results in the workspace, which
 // a second launch joins in a fixed order (no atomics: repeats are bit-identical).
 //
-// Bound by reading the cache where there are few rows: 64 sequences of 16384
-// tokens at most, 8 heads of 128 channels: 177 us, 6.2 TB/s; one of 131072 tokens 56 us,
-// 4.8 TB/s, of which 13 us are the two launches, planning and the join.
+// Bound by reading the cache where there are few rows: 64 sequences of 16384 tokens
+// at most, 8 heads of 128 channels, 1.1 GB: 174 us, 6.3 TB/s, among passes over other
+// caches; 198 us, 5.5 TB/s, behind a pass that leaves L2 full of written lines. One
+// sequence of 131072 tokens 55 us, 4.9 TB/s, of which 12 us are the two launches,
+// planning and the join.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -63,15 +65,15 @@ __device__ int g_cache_attn_error = 0;
 
 constexpr int kSegs = 64;           // segments a CTA plans at a time
 // What a problem costs besides its tiles, in tiles: its rows are loaded and split, its results joined and stored.
-// 64 sequences of 16384 tokens, one query each (8 KV heads, group 4, d = 128): 224 us at 0, 190 at 4, 178 at 8, 180 at
-// 16; of 2048 tokens 111, 61, 50, 53. Tiles of 128 rows (3 chunks of up to 1024 queries, d = 128): 543 us at 3, 528 at
-// 4, 506 at 6, 512 at 8.
+// 64 sequences of up to 16384 tokens, one query each (8 KV heads, group 4): 224 us at 0, 188 at 4, 174 at 8, 177 at 12,
+// 178 at 16; d = 64: 199, 170, 146, 148, 151; of up to 2048 tokens (d = 128): 108, 59, 47, 49, 50. Tiles of 128 rows
+// (3 chunks of up to 1024 queries, d = 128): 532 us at 2, 506 at 4, 493 at 6, 498 at 8, 508 at 12.
 template <int N>
 constexpr int kSegCost = N == 128 ? 6 : 8;
 // A P above 2^kPTop moves the reference maximum, and is 2^kPLog2 then: the further apart, the less often, and the less of
-// P's range lies below. (Trees of 8 tokens on 8 sequences of up to 16384, 32 rows a KV head: 60 us with 13, 54 with 11,
-// 49 with 10, 48 with 9; 64 sequences of up to 2048, one token: 50, 49, 47 and 46.) kPTop is below the largest E5M2
-// (57344) and fp16.
+// P's range lies below. (Trees of 8 tokens on 8 sequences of up to 16384, 32 rows a KV head: 61 us with 13, 49 with 10,
+// 48 with 7; 64 sequences of up to 2048, one token: 50, 47 and 47; chunks of many rows, d = 128: 536, 493 and 484.)
+// kPTop is below the largest E5M2 (57344) and fp16.
 constexpr float kPLog2 = 10.f;
 constexpr float kPTop = 15.75f;
 // What P1 leaves is at most 2^12, what P2 leaves of that 2^8: scaled into E5M2's range, the terms reach further down.
@@ -92,8 +94,8 @@ enum : int {
 // ---------------------------------------------------------------------------
 // Descriptor with F32 accumulate; type 0: E4M3 of kind::f8f6f4, fp16 of kind::f16, 1: E5M2. major 1: MN.
 __host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn, int b_type = 0) {
-  return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+  return (1u << 4) | (static_cast<uint32_t>(b_type) << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t swz_of(int row_bytes) { return row_bytes == 128 ? 2u : (row_bytes == 64 ? 4u : 6u); }
 // 16-byte chunks of a row permuted as the 128-, 64- or 32-byte swizzle does.
@@ -275,8 +277,8 @@ struct Cfg {
   static constexpr int kTile = 128 * D;                    // bytes of a K or V tile
   // The four softmax warpgroups: kPar of them take the tiles in turn, kHalves share a tile's query rows. A tile of 16
   // rows and 64 channels is little work behind a long chain of waits, so more of them go at once (batch of 64 at 16384
-  // tokens: 146 us with four and one, 152 with two and two; at 128 channels 178 and 177, one sequence of 131072 58
-  // and 56).
+  // tokens: 146 us with four and one, 152 with two and two; at 128 channels 178 and 174, one sequence of 131072 57
+  // and 55, 64 of up to 2048 50 and 47).
   static constexpr int kPar = N == 16 && D == 64 ? 4 : 2, kHalves = 4 / kPar;
   static constexpr int kPP = 4 * N;                        // row pitch of a P tile: a key's three terms, N bytes each
   static constexpr int kPTile = 128 * kPP;
@@ -352,7 +354,8 @@ __device__ __forceinline__ Entry entry_of(const Params& p, int e) {
 
 // One role's bounded waits: after one has failed the others return at once. A
 // thread that waits is suspended for up to kNapNs at a time, so that roles with
-// nothing to do leave the issue slots to the softmax warps.
+// nothing to do leave the issue slots to the softmax warps. (How long does not show: 0, 1000 and 200000 measure the
+// same within 0.5 us on batches, trees and chunks.)
 constexpr uint32_t kNapNs = 20000;
 __device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
   uint32_t ok;
@@ -1269,9 +1272,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::kThreads, 1) cache_attn_kernel(cons
 // the keys and nothing is agreed on between warps. The softmax bounds it: 16384
 // exponentials a tile are 1024 cycles of the special-function units and the
 // products 1024 of the tensor core (d = 128), and two softmax warps a scheduler do not
-// cover their latencies. A tree of 61 tokens, group 4, on 8 sequences of up to 16384:
-// 158 us, 0.30 of the measured bf16 rate; 3 chunks of up to 1024 queries at up to 16384
-// tokens, d = 64: 451 us, d = 128: 491 us.
+// cover their latencies: a tile takes 3700 cycles, at 0.40 instructions a cycle and
+// scheduler. A tree of 61 tokens, group 4, on 8 sequences of up to 16384: 158 us (164
+// behind a pass that leaves L2 full of written lines), 0.30 of the measured bf16 rate; 3
+// chunks of up to 1024 queries at up to 16384 tokens, d = 64: 448 us, d = 128: 492 us.
 // Measured against it on the chunks (d = 64; P was two 8-bit terms then): 16 warps with
 // two threads a row 531 us against 503; one S, P beside it 510; each half of the keys with
 // its own S products 522; the exponentials of 32 keys beside the scores of the next 32 709.
@@ -1833,11 +1837,11 @@ bool make_map(CUtensorMap* m, const void* base, const KvCache& c) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows a tile: the smallest that holds a KV head's rows of a sequence; 128
-// is the kernel with the rows on the tensor core's rows. (64 sequences, 4 rows a
-// KV head: 190 us with 16, 209 with 32. 8 sequences of 16384 tokens: 20 and 32
-// rows 54 and 53 us with 32, 84 and 77 with 128; 36 and 64 rows 91 and 82 us as two
-// tiles of 32, 83 and 70 as one of 128.)
+// Query rows a tile: the smallest that holds a KV head's rows of a sequence; 128 is the kernel with the rows on the
+// tensor core's rows. 64 sequences, 4 rows a KV head: 174 us with 16, 185 with 32 (d = 64: 146 and 166). 8 sequences
+// of up to 16384 tokens: 16 rows 48 and 51 us (d = 64: 46 and 47); 20 and 32 rows 50 and 49 us with 32, 84 and 75 with
+// 128 (d = 64: 48 and 46, 76 and 67); 36 and 64 rows 82 and 69 us as one tile of 128, 80 and 68 as two of 32 (d = 64: 74
+// and 60, 77 and 63); 16 sequences with 64 query heads a KV head 141 and 136: one tile or two is even there.
 int rows_a_tile(const CacheAttnArgs& a) {
   const long long rows = static_cast<long long>(a.Tmax) * (a.Hq / a.cache.H);
   return rows <= 16 ? 16 : (rows <= 32 ? 32 : 128);
